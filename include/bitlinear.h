@@ -134,6 +134,57 @@ int bitlinear_quant_act(const void* x, int x_dtype, int M, int K, int8_t* xq, fl
 int bitlinear_rmsnorm_quant(const void* x, int x_dtype, int M, int K, const float* gain, float eps, void* x_norm,
                             int8_t* xq, float* scale, int32_t* rowsum, void* stream);
 
+/*
+ * The residual sum in front of a normalisation, the normalisation and its
+ * activation quantisation in one pass: what every block of a pre-norm model
+ * does between one BitLinear and the next.
+ *   z = x + residual (fp32 sum, rounded to x_dtype and stored), and then
+ *   exactly bitlinear_rmsnorm_quant of z, bit for bit.
+ *   x, residual  device [M][K] of x_dtype (BL_F32 or BL_BF16); 16-byte aligned.
+ *   z            device [M][K] of x_dtype out; may be x or residual itself
+ *                (the sum in place), and otherwise overlaps neither.
+ *   gain, eps, x_norm, xq, scale, rowsum: as bitlinear_rmsnorm_quant
+ *                (x_norm, xq, scale and rowsum overlap no other argument).
+ * No workspace.  Every pointer must be memory of the current device.
+ * Errors: as bitlinear_rmsnorm_quant.
+ */
+int bitlinear_add_rmsnorm_quant(const void* x, const void* residual, int x_dtype, int M, int K, const float* gain,
+                                float eps, void* z, void* x_norm, int8_t* xq, float* scale, int32_t* rowsum,
+                                void* stream);
+
+/* Workspace bytes bitlinear_add_rmsnorm_backward needs when dgain is asked for. */
+size_t bitlinear_add_rmsnorm_backward_workspace_bytes(int M, int K, int z_dtype);
+
+/*
+ * The gradient of bitlinear_add_rmsnorm_quant (and of bitlinear_rmsnorm_quant,
+ * z being its x), for training with latent weights: the quantisation counts
+ * as the identity (the straight-through estimator), so the gradient of the
+ * normalised activations is the dx of the BitLinears that read their codes
+ * (bitlinear_ste_backward).  With r as in the forward, n = z * r and
+ * gd = dnorm * gain:
+ *   dz    = r * (gd - n * mean_k(gd * n)) + dz_in
+ *   dgain = sum over tokens of dnorm * n
+ * in fp32 (the squares of z in double); dz is rounded once.
+ *   z       device [M][K] of z_dtype: the forward's z.
+ *   dnorm   device [M][K] of dnorm_dtype (BL_F32 or BL_BF16): the gradient of
+ *           the normalised activations.
+ *   gain, eps: the forward's (gain NULL for 1).
+ *   dz_in   device [M][K] of z_dtype, or NULL: the gradient that reaches z
+ *           past the norm (the residual stream's).
+ *   dz      device [M][K] of z_dtype out: the gradient of x and of residual
+ *           alike; may be dz_in itself, and otherwise overlaps no input.
+ *   dgain   device fp32 [K] out, or NULL to skip; needs a gain.  The sum's
+ *           order is fixed by the sizes and the device, so results are
+ *           reproducible.  M == 0 writes zeros.
+ *   workspace / workspace_bytes: >= bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, z_dtype)
+ *           when dgain is asked for, else not used (may be NULL).  Its first
+ *           256 bytes are left as they are.
+ * Every pointer must be memory of the current device.
+ */
+int bitlinear_add_rmsnorm_backward(const void* z, int z_dtype, const void* dnorm, int dnorm_dtype, int M, int K,
+                                   const float* gain, float eps, const void* dz_in, void* dz, float* dgain,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* The FFN's gated activation (see bitlinear_glu_quant). */
 typedef enum { BL_GLU_RELU2 = 0, BL_GLU_SILU = 1 } bl_glu;
 

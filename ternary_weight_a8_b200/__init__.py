@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import Sequence
 
@@ -73,6 +74,10 @@ def lib() -> ctypes.CDLL:
             "bitlinear_pack_weights": (i32, [vp, i32, i32, vp, vp, vp, sz, vp]),
             "bitlinear_quant_act": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
             "bitlinear_rmsnorm_quant": (i32, [vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp]),
+            "bitlinear_add_rmsnorm_quant": (i32, [vp, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp]),
+            "bitlinear_add_rmsnorm_backward_workspace_bytes": (sz, [i32, i32, i32]),
+            "bitlinear_add_rmsnorm_backward": (i32, [vp, i32, vp, i32, i32, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz,
+                                                     vp]),
             "bitlinear_glu_quant": (i32, [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]),
             "bitlinear_gate_up_glu_workspace_bytes": (sz, [i32, i32, i32]),
             "bitlinear_gate_up_glu": (i32, [vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
@@ -238,6 +243,134 @@ def rmsnorm_quant(x: torch.Tensor, gain: torch.Tensor | None = None, eps: float 
     _check(lib().bitlinear_rmsnorm_quant(_ptr(x), _dtype_code(x.dtype), M, K, _ptr(gain), float(eps), _ptr(norm),
                                          _ptr(xq), _ptr(scale), _ptr(rowsum), _stream(stream)))
     return (norm, xq, scale, rowsum) if norm is not None else (xq, scale, rowsum)
+
+
+_WS_LOCAL = threading.local()
+
+
+class _Call:
+    """One library call's device, stream and buffers.
+
+    The call's tensors must share one CUDA device and be contiguous; the call
+    runs with that device current, on ``stream`` or its current stream.
+    Outputs and workspaces that the call makes itself belong to that stream;
+    the caller's tensors are recorded on it when it is not the current one, so
+    that the allocator gives none of them away too early."""
+
+    __slots__ = ("dev", "stream", "handle", "_other", "_switch")
+
+    def __init__(self, x: torch.Tensor, stream):
+        if not x.is_cuda:
+            raise ValueError("tensor must be on a CUDA device")
+        self.dev = x.device
+        current = torch.cuda.current_stream(self.dev)
+        if stream is not None and stream.device != self.dev:
+            raise ValueError("stream of %s for tensors of %s" % (stream.device, self.dev))
+        self.stream = current if stream is None else stream
+        self._other = self.stream.cuda_stream != current.cuda_stream
+        self._switch = self.dev.index != torch.cuda.current_device()
+        self.handle = self.stream.cuda_stream
+
+    def ptr(self, t: torch.Tensor | None, name: str, shape: tuple | None = None, dtype=None):
+        """The address of an argument, its place, layout, shape and type checked (None for an absent one)."""
+        if t is None:
+            return None
+        if t.device != self.dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, self.dev))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s has shape %s: need %s" % (name, tuple(t.shape), tuple(shape)))
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("%s has dtype %s: need %s" % (name, t.dtype, dtype))
+        if self._other:
+            t.record_stream(self.stream)
+        return t.data_ptr()
+
+    def new(self, shape, dtype, zero: bool = False) -> torch.Tensor:
+        """An output of the call, from its stream's memory."""
+        make = torch.zeros if zero else torch.empty
+        if not self._other:
+            return make(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            t = make(shape, dtype=dtype, device=self.dev)
+        t.record_stream(torch.cuda.current_stream(self.dev))  # the caller may use it there
+        return t
+
+    def workspace(self, nbytes: int) -> torch.Tensor:
+        """The workspace of a call that was given none: one cached per host thread, device and stream (the launches
+        of calls that two threads make on one stream may interleave), or, while the stream is being captured, one
+        of the graph's own (graphs may be replayed side by side, and outlive the cached one)."""
+        if self._other or self._switch:
+            with torch.cuda.stream(self.stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            return self.new((max(int(nbytes), 256),), torch.uint8, zero=True)
+        cache = _WS_LOCAL.__dict__
+        key = (self.dev.index, self.handle)
+        ws = cache.get(key)
+        if ws is None or ws.numel() < nbytes:
+            with torch.cuda.stream(self.stream):
+                ws = cache[key] = new_workspace(nbytes, self.dev)
+        return ws
+
+    def run(self, fn, *args) -> None:
+        if self._switch:
+            with torch.cuda.device(self.dev):
+                _check(fn(*args, self.handle))
+        else:
+            _check(fn(*args, self.handle))
+
+
+def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, gain: torch.Tensor | None = None, eps: float = 1e-6,
+                      z: torch.Tensor | None = None, x_norm=None, xq=None, scale=None, rowsum=None, stream=None):
+    """z = x + residual, RMSNorm of z and its per-token quantisation in one pass: returns (z, xq, scale, rowsum),
+    with the normalised activations after z when ``x_norm`` is True or a tensor.  ``z`` may be ``x`` or
+    ``residual`` (the sum in place).  The codes equal ``rmsnorm_quant``'s on z."""
+    M, K = x.shape
+    dt = x.dtype
+    code = _dtype_code(dt)
+    c = _Call(x, stream)
+    z = c.new((M, K), dt) if z is None else z
+    xq = c.new((M, K), torch.int8) if xq is None else xq
+    scale = c.new((M,), torch.float32) if scale is None else scale
+    rowsum = c.new((M,), torch.int32) if rowsum is None else rowsum
+    norm = c.new((M, K), dt) if x_norm is True else (x_norm if isinstance(x_norm, torch.Tensor) else None)
+    c.run(lib().bitlinear_add_rmsnorm_quant, c.ptr(x, "x"), c.ptr(residual, "residual", (M, K), dt), code, M, K,
+          c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(z, "z", (M, K), dt),
+          c.ptr(norm, "x_norm", (M, K), dt), c.ptr(xq, "xq", (M, K), torch.int8),
+          c.ptr(scale, "scale", (M,), torch.float32), c.ptr(rowsum, "rowsum", (M,), torch.int32))
+    return (z, norm, xq, scale, rowsum) if norm is not None else (z, xq, scale, rowsum)
+
+
+def add_rmsnorm_backward_workspace_bytes(M: int, K: int, z_dtype: torch.dtype) -> int:
+    return int(lib().bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, _dtype_code(z_dtype)))
+
+
+def add_rmsnorm_backward(z: torch.Tensor, dnorm: torch.Tensor, gain: torch.Tensor | None = None, eps: float = 1e-6,
+                         dz_in: torch.Tensor | None = None, dz: torch.Tensor | None = None, dgain=True,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of ``add_rmsnorm_quant`` (the quantisation as the identity): from z, the gradient ``dnorm`` of
+    the normalised activations and the gradient ``dz_in`` that reaches z past the norm, returns (dz, dgain).  dz
+    is the gradient of x and of the residual alike and may be ``dz_in``; dgain is None without a gain, or when
+    ``dgain`` is False; it is written to ``dgain`` when that is a tensor."""
+    M, K = z.shape
+    code, dcode = _dtype_code(z.dtype), _dtype_code(dnorm.dtype)
+    c = _Call(z, stream)
+    dz = c.new((M, K), z.dtype) if dz is None else dz
+    if dgain is True:
+        dgt = c.new((K,), torch.float32) if gain is not None else None
+    else:
+        dgt = dgain if isinstance(dgain, torch.Tensor) else None
+    if dgt is not None and workspace is None:
+        workspace = c.workspace(lib().bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, code))
+    c.run(lib().bitlinear_add_rmsnorm_backward, c.ptr(z, "z"), code, c.ptr(dnorm, "dnorm", (M, K)), dcode, M, K,
+          c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(dz_in, "dz_in", (M, K), z.dtype),
+          c.ptr(dz, "dz", (M, K), z.dtype), c.ptr(dgt, "dgain", (K,), torch.float32), c.ptr(workspace, "workspace"),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return dz, dgt
 
 
 def forward_lut(packed: torch.Tensor, gamma: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,

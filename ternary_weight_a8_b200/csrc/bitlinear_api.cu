@@ -60,6 +60,65 @@ int check_ptr(const void* p, const char* name, size_t align, bool nullable = fal
   return BL_OK;
 }
 
+// As check_ptr, and device memory must be the current device's (a kernel of
+// this device would otherwise run on another's memory, or fault).
+int check_here(const void* p, const char* name, size_t align, bool nullable = false) {
+  if (p == nullptr) {
+    if (nullable) return BL_OK;
+    return fail(BL_ERR_INVALID_ARG, "%s is NULL", name);
+  }
+  if (reinterpret_cast<uintptr_t>(p) % align != 0) {
+    return fail(BL_ERR_MISALIGNED, "%s (%p) is not %zu-byte aligned", name, p, align);
+  }
+  cudaPointerAttributes attr;
+  cudaError_t e = cudaPointerGetAttributes(&attr, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(BL_ERR_INVALID_ARG, "%s (%p): cudaPointerGetAttributes failed: %s", name, p, cudaGetErrorString(e));
+  }
+  if (attr.type == cudaMemoryTypeUnregistered || (attr.type == cudaMemoryTypeHost && attr.devicePointer == nullptr)) {
+    return fail(BL_ERR_INVALID_ARG, "%s (%p) is not device-accessible memory", name, p);
+  }
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (attr.type == cudaMemoryTypeDevice && attr.device != dev) {
+    return fail(BL_ERR_INVALID_ARG, "%s (%p) is memory of device %d; the current device is %d", name, p, attr.device,
+                dev);
+  }
+  return BL_OK;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+// `out` must not overlap any of the `n` other buffers (absent ones are
+// skipped); with `same`, it may be exactly that buffer.
+int check_apart(const Span& out, const Span* others, int n, bool same = false) {
+  if (!out.p) return BL_OK;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(out.p);
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t b0 = reinterpret_cast<uintptr_t>(others[i].p);
+    if (!others[i].p || (same && a0 == b0)) continue;
+    if (a0 < b0 + others[i].bytes && b0 < a0 + out.bytes)
+      return fail(BL_ERR_INVALID_ARG, "%s overlaps %s", out.name, others[i].name);
+  }
+  return BL_OK;
+}
+
+int check_k(int K) {
+  if (K < 64 || K % 64 != 0) return fail(BL_ERR_UNSUPPORTED_SHAPE, "K = %d: need K >= 64 and K %% 64 == 0", K);
+  return BL_OK;
+}
+
+int check_eps(float eps) {
+  if (!(eps >= 0.0f) || !(eps < INFINITY)) return fail(BL_ERR_INVALID_ARG, "eps = %g: need a finite eps >= 0", eps);
+  return BL_OK;
+}
+
 int check_dtype(int t, const char* name) {
   if (t != BL_F32 && t != BL_BF16) return fail(BL_ERR_INVALID_ARG, "%s: unknown dtype %d", name, t);
   return BL_OK;
@@ -317,6 +376,86 @@ int bitlinear_rmsnorm_quant(const void* x, int x_dtype, int M, int K, const floa
   cudaError_t e = bl::launch_rmsnorm_quant(x, x_dtype == BL_BF16, M, K, gain, eps, x_norm, xq, scale, rowsum,
                                            static_cast<cudaStream_t>(stream), true);
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm_quant launch");
+  return BL_OK;
+}
+
+int bitlinear_add_rmsnorm_quant(const void* x, const void* residual, int x_dtype, int M, int K, const float* gain,
+                                float eps, void* z, void* x_norm, int8_t* xq, float* scale, int32_t* rowsum,
+                                void* stream) {
+  BL_TRY(check_dtype(x_dtype, "x_dtype"));
+  if (M < 0) return fail(BL_ERR_INVALID_ARG, "M = %d < 0", M);
+  BL_TRY(check_k(K));
+  BL_TRY(check_eps(eps));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_here(x, "x", 16));
+  BL_TRY(check_here(residual, "residual", 16));
+  BL_TRY(check_here(gain, "gain", 16, true));
+  BL_TRY(check_here(z, "z", 16));
+  BL_TRY(check_here(x_norm, "x_norm", 16, true));
+  BL_TRY(check_here(xq, "xq", 16));
+  BL_TRY(check_here(scale, "scale", 4));
+  BL_TRY(check_here(rowsum, "rowsum", 4, true));
+  const size_t row = static_cast<size_t>(K), mk = static_cast<size_t>(M) * row * (x_dtype == BL_BF16 ? 2 : 4);
+  const Span sp[] = {{x, mk, "x"},           {residual, mk, "residual"},
+                     {gain, row * 4, "gain"}, {z, mk, "z"},
+                     {x_norm, mk, "x_norm"},  {xq, static_cast<size_t>(M) * row, "xq"},
+                     {scale, static_cast<size_t>(M) * 4, "scale"}, {rowsum, static_cast<size_t>(M) * 4, "rowsum"}};
+  BL_TRY(check_apart(sp[3], sp, 2, true));
+  BL_TRY(check_apart(sp[3], sp + 2, 1));
+  for (int i = 4; i < 8; ++i) BL_TRY(check_apart(sp[i], sp, i));
+  cudaError_t e = bl::launch_add_rmsnorm_quant(x, residual, x_dtype == BL_BF16, M, K, gain, eps, z, x_norm, xq, scale,
+                                               rowsum, static_cast<cudaStream_t>(stream), true);
+  if (e != cudaSuccess) return cuda_fail(e, "add_rmsnorm_quant launch");
+  return BL_OK;
+}
+
+size_t bitlinear_add_rmsnorm_backward_workspace_bytes(int M, int K, int z_dtype) {
+  if (M < 0 || K < 0) return 0;
+  return kStatusBytes + bl::add_rmsnorm_backward_scratch_bytes(M, K, z_dtype == BL_BF16);
+}
+
+int bitlinear_add_rmsnorm_backward(const void* z, int z_dtype, const void* dnorm, int dnorm_dtype, int M, int K,
+                                   const float* gain, float eps, const void* dz_in, void* dz, float* dgain,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  BL_TRY(check_dtype(z_dtype, "z_dtype"));
+  BL_TRY(check_dtype(dnorm_dtype, "dnorm_dtype"));
+  if (M < 0) return fail(BL_ERR_INVALID_ARG, "M = %d < 0", M);
+  BL_TRY(check_k(K));
+  BL_TRY(check_eps(eps));
+  if (dgain && !gain) return fail(BL_ERR_INVALID_ARG, "dgain without a gain");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (!dgain) return BL_OK;
+    BL_TRY(check_here(dgain, "dgain", 16));
+    cudaError_t e = cudaMemsetAsync(dgain, 0, static_cast<size_t>(K) * 4, s);  // a sum over no tokens
+    return e == cudaSuccess ? BL_OK : cuda_fail(e, "clearing dgain");
+  }
+  BL_TRY(check_here(z, "z", 16));
+  BL_TRY(check_here(dnorm, "dnorm", 16));
+  BL_TRY(check_here(gain, "gain", 16, true));
+  BL_TRY(check_here(dz_in, "dz_in", 16, true));
+  BL_TRY(check_here(dz, "dz", 16));
+  BL_TRY(check_here(dgain, "dgain", 16, true));
+  const size_t mk = static_cast<size_t>(M) * K, kb = static_cast<size_t>(K) * 4;
+  const size_t zb = mk * (z_dtype == BL_BF16 ? 2 : 4), db = mk * (dnorm_dtype == BL_BF16 ? 2 : 4);
+  const Span in[] = {{z, zb, "z"}, {dnorm, db, "dnorm"}, {gain, kb, "gain"}, {dz_in, zb, "dz_in"}, {dz, zb, "dz"}};
+  BL_TRY(check_apart(in[4], in, 3));
+  BL_TRY(check_apart(in[4], in + 3, 1, true));
+  BL_TRY(check_apart({dgain, kb, "dgain"}, in, 5));
+  uint8_t* scratch = nullptr;
+  if (dgain) {
+    BL_TRY(check_here(workspace, "workspace", 256));
+    const size_t need = bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, z_dtype);
+    if (workspace_bytes < need)
+      return fail(BL_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+    BL_TRY(check_apart({workspace, need, "workspace"}, in, 5));
+    const Span ws{workspace, need, "workspace"};
+    BL_TRY(check_apart({dgain, kb, "dgain"}, &ws, 1));
+    scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+  }
+  cudaError_t e = bl::launch_add_rmsnorm_backward(z, z_dtype == BL_BF16, dnorm, dnorm_dtype == BL_BF16, M, K, gain, eps,
+                                                  dz_in, dz, dgain, scratch, s);
+  if (e != cudaSuccess) return cuda_fail(e, "add_rmsnorm_backward launch");
   return BL_OK;
 }
 

@@ -74,6 +74,19 @@ cudaError_t launch_act_quant_group(const QuantArgs* items, int n_items, int M, i
 cudaError_t launch_rmsnorm_quant(const void* x, int x_bf16, int M, int K, const float* gain, float eps, void* x_norm,
                                  int8_t* xq, float* scale, int32_t* rowsum, cudaStream_t stream, bool pdl);
 
+// The residual sum z = x + residual, RMSNorm of z and its quantisation (z may
+// be x or residual; x_norm and rowsum optional).
+cudaError_t launch_add_rmsnorm_quant(const void* x, const void* residual, int x_bf16, int M, int K, const float* gain,
+                                     float eps, void* z, void* x_norm, int8_t* xq, float* scale, int32_t* rowsum,
+                                     cudaStream_t stream, bool pdl);
+// Its gradient: dz from the gradient of the normalised activations and dz_in
+// (optional; dz may be dz_in), dgain [K] (null to skip).  scratch (needed for
+// dgain): add_rmsnorm_backward_scratch_bytes bytes, 256-byte aligned.
+size_t add_rmsnorm_backward_scratch_bytes(int M, int K, int z_bf16);
+cudaError_t launch_add_rmsnorm_backward(const void* z, int z_bf16, const void* dnorm, int dnorm_bf16, int M, int K,
+                                        const float* gain, float eps, const void* dz_in, void* dz, float* dgain,
+                                        uint8_t* scratch, cudaStream_t stream);
+
 // The FFN's gated activation h = act(gate) * up fused with the per-token
 // quantisation of h (the down BitLinear's input); h (optional) written in the
 // activation type.
