@@ -332,6 +332,47 @@ int bitlinear_forward_quantized(const uint8_t* packed, const float* gamma, int N
                                 int M, void* y, int y_dtype, int32_t* acc_out, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* Workspace bytes bitlinear_forward_i8 needs (status word + q, s). */
+size_t bitlinear_i8_workspace_bytes(int M, int N, int K);
+
+/*
+ * The 8-bit product for the layers of a ternary model that are not ternary
+ * (the embedding matrix as output head, say: "BitNet b1.58 and the 1-Bit AI
+ * Architecture Revolution", section "Empirical Performance and The New
+ * Scaling Law", embeddings at a higher precision), on the same activation
+ * codes as the BitLinears: int8 codes on both sides, a scale for each token
+ * and each output channel, int32 accumulation.
+ *   acc[m][n] = sum_k q[m][k] * wq[n][k]                       (exact)
+ *   y[m][n]   = fp32(acc) * ((1 / s[m]) * (1 / wscale[n]))     (fp32, then y_dtype)
+ *   wq      device int8 [N][K]; wscale device fp32 [N]: row n stands for
+ *           wq[n][k] / wscale[n].  bitlinear_quant_act of the weights, a row
+ *           for a token, writes both (any codes in [-128, 127] do).
+ *   x       device [M][K] of x_dtype, quantised per token by the call.
+ *   y       device [M][N] of y_dtype out; any N >= 1.
+ *   acc_out device int32 [M][N] out, or NULL: the exact accumulators.
+ *   workspace / workspace_bytes: >= bitlinear_i8_workspace_bytes(M, N, K),
+ *           its first 256 bytes zero.
+ * K <= 131008 (the int32 sums).  M <= 32 streams the weights through a decode
+ * kernel; larger M runs on the tensor cores (tcgen05); bitlinear_set_path
+ * forces either (its GEMV takes M <= 32 here).  Both give the same
+ * accumulators and outputs, bit for bit.  Unlike the packed weights of the
+ * other products, wq may be written by the kernel just before the call.
+ * y, acc_out and the workspace overlap no other argument.  Every pointer
+ * must be memory of the current device.
+ */
+int bitlinear_forward_i8(const int8_t* wq, const float* wscale, int N, int K, const void* x, int x_dtype, int M, void* y,
+                         int y_dtype, int32_t* acc_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same on activations already quantised (xq [M][K], scale [M], as
+ * bitlinear_quant_act, bitlinear_rmsnorm_quant, bitlinear_add_rmsnorm_quant or
+ * bitlinear_glu_quant wrote them; no code sums needed).  Only the
+ * workspace's status word is used (256 bytes suffice).
+ */
+int bitlinear_forward_i8_quantized(const int8_t* wq, const float* wscale, int N, int K, const int8_t* xq,
+                                   const float* scale, int M, void* y, int y_dtype, int32_t* acc_out, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /*
  * One BitLinear of a chain: weights, gamma, shape, input [M][K], output [M][N].
  *   x       device [M][K] activations of the chain's x_dtype; ignored (may be
@@ -427,7 +468,10 @@ int bitlinear_forward_noalloc(const uint8_t* packed, const float* gamma, int N, 
  */
 int bitlinear_noalloc_status(void* stream);
 
-/* Forces the product kernel: 0 = by M (default), 1 = GEMV (M <= 16 only), 2 = GEMM.  Per thread. */
+/*
+ * Forces the product kernel: 0 = by M (default), 1 = GEMV (M <= 16 only; M <= 32
+ * for the 8-bit product), 2 = GEMM.  Per thread.
+ */
 int bitlinear_set_path(int path);
 
 /*

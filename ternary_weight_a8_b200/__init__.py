@@ -87,6 +87,9 @@ def lib() -> ctypes.CDLL:
             "bitlinear_workspace_bytes": (sz, [i32, i32, i32]),
             "bitlinear_forward": (i32, [vp, vp, i32, i32, vp, i32, i32, vp, i32, vp, vp, sz, vp]),
             "bitlinear_forward_quantized": (i32, [vp, vp, i32, i32, vp, vp, vp, i32, vp, i32, vp, vp, sz, vp]),
+            "bitlinear_i8_workspace_bytes": (sz, [i32, i32, i32]),
+            "bitlinear_forward_i8": (i32, [vp, vp, i32, i32, vp, i32, i32, vp, i32, vp, vp, sz, vp]),
+            "bitlinear_forward_i8_quantized": (i32, [vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]),
             "bitlinear_chain_workspace_bytes": (sz, [ctypes.POINTER(bl_layer), i32, i32]),
             "bitlinear_layer_chain": (i32, [ctypes.POINTER(bl_layer), i32, i32, i32, i32, vp, sz, vp]),
             "bitlinear_device_status": (i32, [vp, vp]),
@@ -257,68 +260,82 @@ class _Call:
     the caller's tensors are recorded on it when it is not the current one, so
     that the allocator gives none of them away too early."""
 
-    __slots__ = ("dev", "stream", "handle", "_other", "_switch")
+    __slots__ = ("like", "index", "stream", "handle", "switch", "held")
 
     def __init__(self, x: torch.Tensor, stream):
         if not x.is_cuda:
             raise ValueError("tensor must be on a CUDA device")
-        self.dev = x.device
-        current = torch.cuda.current_stream(self.dev)
-        if stream is not None and stream.device != self.dev:
-            raise ValueError("stream of %s for tensors of %s" % (stream.device, self.dev))
-        self.stream = current if stream is None else stream
-        self._other = self.stream.cuda_stream != current.cuda_stream
-        self._switch = self.dev.index != torch.cuda.current_device()
-        self.handle = self.stream.cuda_stream
+        self.like = x
+        self.index = x.get_device()
+        # The current stream's handle without making a Stream object (2 us of a 15 us call).
+        self.handle = torch._C._cuda_getCurrentRawStream(self.index)
+        self.switch = self.index != torch.cuda.current_device()
+        self.stream = None  # set when it is another stream than the current one
+        if stream is not None:
+            if stream.device.index != self.index:
+                raise ValueError("stream of %s for tensors of %s" % (stream.device, x.device))
+            if stream.cuda_stream != self.handle:
+                self.stream, self.handle = stream, stream.cuda_stream
 
     def ptr(self, t: torch.Tensor | None, name: str, shape: tuple | None = None, dtype=None):
-        """The address of an argument, its place, layout, shape and type checked (None for an absent one)."""
+        """The address of a caller's tensor, its place, layout, shape and type checked (None for an absent one)."""
         if t is None:
             return None
-        if t.device != self.dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, self.dev))
+        if t.get_device() != self.index:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, self.like.device))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
         if shape is not None and t.shape != shape:
             raise ValueError("%s has shape %s: need %s" % (name, tuple(t.shape), tuple(shape)))
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise ValueError("%s has dtype %s: need %s" % (name, t.dtype, dtype))
-        if self._other:
+        if self.stream is not None:
             t.record_stream(self.stream)
         return t.data_ptr()
 
     def new(self, shape, dtype, zero: bool = False) -> torch.Tensor:
         """An output of the call, from its stream's memory."""
-        make = torch.zeros if zero else torch.empty
-        if not self._other:
-            return make(shape, dtype=dtype, device=self.dev)
+        make = self.like.new_zeros if zero else self.like.new_empty
+        if self.stream is None:
+            return make(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            t = make(shape, dtype=dtype, device=self.dev)
-        t.record_stream(torch.cuda.current_stream(self.dev))  # the caller may use it there
+            t = make(shape, dtype=dtype)
+        t.record_stream(torch.cuda.current_stream(self.index))  # the caller may use it there
         return t
 
-    def workspace(self, nbytes: int) -> torch.Tensor:
-        """The workspace of a call that was given none: one cached per host thread, device and stream (the launches
-        of calls that two threads make on one stream may interleave), or, while the stream is being captured, one
-        of the graph's own (graphs may be replayed side by side, and outlive the cached one)."""
-        if self._other or self._switch:
-            with torch.cuda.stream(self.stream):
+    def out(self, t: torch.Tensor | None, name: str, shape: tuple, dtype):
+        """An output and its address: the caller's tensor, checked, or a new one."""
+        if t is None:
+            t = self.new(shape, dtype)
+            return t, t.data_ptr()
+        return t, self.ptr(t, name, shape, dtype)
+
+    def workspace(self, ws: torch.Tensor | None, nbytes: int):
+        """The address and size of a call's workspace.  Without a caller's: one cached per host thread, device and
+        stream (the launches of calls that two threads make on one stream may interleave), or, while the stream is
+        being captured, one of the graph's own (graphs may be replayed side by side, and outlive the cached one)."""
+        if ws is not None:
+            return self.ptr(ws, "workspace"), ws.numel() * ws.element_size()
+        if self.stream is not None or self.switch:
+            with torch.cuda.stream(self.stream or torch.cuda.current_stream(self.index)):
                 capturing = torch.cuda.is_current_stream_capturing()
         else:
             capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
-            return self.new((max(int(nbytes), 256),), torch.uint8, zero=True)
-        cache = _WS_LOCAL.__dict__
-        key = (self.dev.index, self.handle)
-        ws = cache.get(key)
-        if ws is None or ws.numel() < nbytes:
-            with torch.cuda.stream(self.stream):
-                ws = cache[key] = new_workspace(nbytes, self.dev)
-        return ws
+            ws = self.new((max(int(nbytes), 256),), torch.uint8, zero=True)
+        else:
+            cache = _WS_LOCAL.__dict__
+            key = (self.index, self.handle)
+            ws = cache.get(key)
+            if ws is None or ws.numel() < nbytes:
+                with torch.cuda.stream(self.stream or torch.cuda.current_stream(self.index)):
+                    ws = cache[key] = new_workspace(nbytes, self.like.device)
+        self.held = ws  # until the launches are made
+        return ws.data_ptr(), ws.numel()
 
     def run(self, fn, *args) -> None:
-        if self._switch:
-            with torch.cuda.device(self.dev):
+        if self.switch:
+            with torch.cuda.device(self.index):
                 _check(fn(*args, self.handle))
         else:
             _check(fn(*args, self.handle))
@@ -333,16 +350,16 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, gain: torch.Tenso
     dt = x.dtype
     code = _dtype_code(dt)
     c = _Call(x, stream)
-    z = c.new((M, K), dt) if z is None else z
-    xq = c.new((M, K), torch.int8) if xq is None else xq
-    scale = c.new((M,), torch.float32) if scale is None else scale
-    rowsum = c.new((M,), torch.int32) if rowsum is None else rowsum
-    norm = c.new((M, K), dt) if x_norm is True else (x_norm if isinstance(x_norm, torch.Tensor) else None)
+    z, zp = c.out(z, "z", (M, K), dt)
+    xq, qp = c.out(xq, "xq", (M, K), torch.int8)
+    scale, sp = c.out(scale, "scale", (M,), torch.float32)
+    rowsum, rp = c.out(rowsum, "rowsum", (M,), torch.int32)
+    norm = npt = None
+    if x_norm is not None and x_norm is not False:
+        norm, npt = c.out(None if x_norm is True else x_norm, "x_norm", (M, K), dt)
     c.run(lib().bitlinear_add_rmsnorm_quant, c.ptr(x, "x"), c.ptr(residual, "residual", (M, K), dt), code, M, K,
-          c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(z, "z", (M, K), dt),
-          c.ptr(norm, "x_norm", (M, K), dt), c.ptr(xq, "xq", (M, K), torch.int8),
-          c.ptr(scale, "scale", (M,), torch.float32), c.ptr(rowsum, "rowsum", (M,), torch.int32))
-    return (z, norm, xq, scale, rowsum) if norm is not None else (z, xq, scale, rowsum)
+          c.ptr(gain, "gain", (K,), torch.float32), float(eps), zp, npt, qp, sp, rp)
+    return (z, xq, scale, rowsum) if norm is None else (z, norm, xq, scale, rowsum)
 
 
 def add_rmsnorm_backward_workspace_bytes(M: int, K: int, z_dtype: torch.dtype) -> int:
@@ -359,18 +376,18 @@ def add_rmsnorm_backward(z: torch.Tensor, dnorm: torch.Tensor, gain: torch.Tenso
     M, K = z.shape
     code, dcode = _dtype_code(z.dtype), _dtype_code(dnorm.dtype)
     c = _Call(z, stream)
-    dz = c.new((M, K), z.dtype) if dz is None else dz
-    if dgain is True:
-        dgt = c.new((K,), torch.float32) if gain is not None else None
-    else:
-        dgt = dgain if isinstance(dgain, torch.Tensor) else None
-    if dgt is not None and workspace is None:
-        workspace = c.workspace(lib().bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, code))
+    dz, op = c.out(dz, "dz", (M, K), z.dtype)
+    gp = wp = None
+    nbytes = 0
+    if dgain is True and gain is None or dgain is False:
+        dgain = None
+    if dgain is not None:
+        dgain, gp = c.out(None if dgain is True else dgain, "dgain", (K,), torch.float32)
+        wp, nbytes = c.workspace(workspace, lib().bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, code))
     c.run(lib().bitlinear_add_rmsnorm_backward, c.ptr(z, "z"), code, c.ptr(dnorm, "dnorm", (M, K)), dcode, M, K,
-          c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(dz_in, "dz_in", (M, K), z.dtype),
-          c.ptr(dz, "dz", (M, K), z.dtype), c.ptr(dgt, "dgain", (K,), torch.float32), c.ptr(workspace, "workspace"),
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    return dz, dgt
+          c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(dz_in, "dz_in", (M, K), z.dtype), op, gp, wp,
+          nbytes)
+    return dz, dgain
 
 
 def forward_lut(packed: torch.Tensor, gamma: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,
@@ -494,6 +511,65 @@ def forward_quantized(packed: torch.Tensor, gamma: torch.Tensor, xq: torch.Tenso
                                              _ptr(rowsum), M, _ptr(y), _dtype_code(y.dtype), _ptr(acc),
                                              _ptr(workspace), workspace.numel(), _stream(stream)))
     return (y, acc) if acc is not None else y
+
+
+def quant_weights_i8(W: torch.Tensor, wq: torch.Tensor | None = None, wscale: torch.Tensor | None = None, stream=None):
+    """Weights ``[N][K]`` (fp32/bf16) -> (int8 wq ``[N][K]``, fp32 wscale ``[N]``) for the 8-bit product: each output
+    channel quantised as ``quant_act`` quantises a token (wscale = 127 / max |W[n]|)."""
+    N, K = W.shape
+    c = _Call(W, stream)
+    wq, qp = c.out(wq, "wq", (N, K), torch.int8)
+    wscale, sp = c.out(wscale, "wscale", (N,), torch.float32)
+    c.run(lib().bitlinear_quant_act, c.ptr(W, "W"), _dtype_code(W.dtype), N, K, qp, sp, None)
+    return wq, wscale
+
+
+def i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().bitlinear_i8_workspace_bytes(M, N, K))
+
+
+def _i8_outputs(c: _Call, M: int, N: int, out_dtype, y, acc_out):
+    """y and acc of an 8-bit product with their addresses and y's type code."""
+    if y is None:
+        code = _dtype_code(out_dtype)
+        y, yp = c.out(None, "y", (M, N), out_dtype)
+    else:
+        code = _dtype_code(y.dtype)
+        yp = c.ptr(y, "y", (M, N))
+    acc = ap = None
+    if acc_out is not None and acc_out is not False:
+        acc, ap = c.out(None if acc_out is True else acc_out, "acc_out", (M, N), torch.int32)
+    return y, yp, code, acc, ap
+
+
+def forward_i8(wq: torch.Tensor, wscale: torch.Tensor, x: torch.Tensor, out_dtype=torch.bfloat16,
+               y: torch.Tensor | None = None, acc_out: torch.Tensor | bool | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """y = x . W^T in 8-bit integers, x (fp32/bf16) quantised per token and W given as codes ``[N][K]`` with a scale
+    for each output channel (``quant_weights_i8``): returns y, or (y, acc) when ``acc_out`` is True or a tensor."""
+    N, K = wq.shape
+    M = x.shape[0]
+    c = _Call(x, stream)
+    y, yp, ycode, acc, ap = _i8_outputs(c, M, N, out_dtype, y, acc_out)
+    wp, nbytes = c.workspace(workspace, lib().bitlinear_i8_workspace_bytes(M, N, K))
+    c.run(lib().bitlinear_forward_i8, c.ptr(wq, "wq", None, torch.int8), c.ptr(wscale, "wscale", (N,), torch.float32), N, K,
+          c.ptr(x, "x", (M, K)), _dtype_code(x.dtype), M, yp, ycode, ap, wp, nbytes)
+    return y if acc is None else (y, acc)
+
+
+def forward_i8_quantized(wq: torch.Tensor, wscale: torch.Tensor, xq: torch.Tensor, scale: torch.Tensor,
+                         out_dtype=torch.bfloat16, y: torch.Tensor | None = None,
+                         acc_out: torch.Tensor | bool | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The 8-bit product on activations already quantised (``quant_act`` or a norm's codes and scales)."""
+    N, K = wq.shape
+    M = xq.shape[0]
+    c = _Call(xq, stream)
+    y, yp, ycode, acc, ap = _i8_outputs(c, M, N, out_dtype, y, acc_out)
+    wp, nbytes = c.workspace(workspace, 256)
+    c.run(lib().bitlinear_forward_i8_quantized, c.ptr(wq, "wq", None, torch.int8),
+          c.ptr(wscale, "wscale", (N,), torch.float32), N, K, c.ptr(xq, "xq", (M, K), torch.int8),
+          c.ptr(scale, "scale", (M,), torch.float32), M, yp, ycode, ap, wp, nbytes)
+    return y if acc is None else (y, acc)
 
 
 @dataclass

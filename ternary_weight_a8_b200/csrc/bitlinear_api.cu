@@ -459,6 +459,81 @@ int bitlinear_add_rmsnorm_backward(const void* z, int z_dtype, const void* dnorm
   return BL_OK;
 }
 
+// The 8-bit product's checks that need no pointer.
+static int check_i8(int N, int K, int M, int y_dtype) {
+  BL_TRY(check_nk(N, K));
+  if (K > bl::kI8MaxK)
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "K = %d: int32 sums of 8-bit products need K <= %d", K, bl::kI8MaxK);
+  BL_TRY(check_dtype(y_dtype, "y_dtype"));
+  if (M < 0) return fail(BL_ERR_INVALID_ARG, "M = %d < 0", M);
+  if (g_path == 1 && M > bl::kI8GemvMaxTokens)
+    return fail(BL_ERR_UNSUPPORTED_SHAPE, "GEMV path forced with M = %d > %d", M, bl::kI8GemvMaxTokens);
+  return BL_OK;
+}
+
+static int launch_i8(const bl::I8Args& a, cudaStream_t s) {
+  const bool gemv = g_path == 1 || (g_path == 0 && a.M <= bl::kI8GemvMaxTokens);
+  cudaError_t e = gemv ? bl::launch_i8_gemv(a, s, true) : bl::launch_i8_gemm(a, s, true);
+  return e == cudaSuccess ? BL_OK : cuda_fail(e, "8-bit product launch");
+}
+
+size_t bitlinear_i8_workspace_bytes(int M, int N, int K) { return bitlinear_workspace_bytes(M, N, K); }
+
+int bitlinear_forward_i8_quantized(const int8_t* wq, const float* wscale, int N, int K, const int8_t* xq,
+                                   const float* scale, int M, void* y, int y_dtype, int32_t* acc_out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  BL_TRY(check_i8(N, K, M, y_dtype));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_here(wq, "wq", 16));
+  BL_TRY(check_here(wscale, "wscale", 4));
+  BL_TRY(check_here(xq, "xq", 16));
+  BL_TRY(check_here(scale, "scale", 4));
+  BL_TRY(check_here(y, "y", 16));
+  BL_TRY(check_here(acc_out, "acc_out", 16, true));
+  BL_TRY(check_here(workspace, "workspace", 256));
+  if (workspace_bytes < kStatusBytes)
+    return fail(BL_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, kStatusBytes);
+  const size_t n = static_cast<size_t>(N), m = static_cast<size_t>(M);
+  const Span sp[] = {{wq, n * K, "wq"}, {wscale, n * 4, "wscale"}, {xq, m * K, "xq"}, {scale, m * 4, "scale"},
+                     {workspace, kStatusBytes, "workspace"}, {y, m * n * (y_dtype == BL_BF16 ? 2 : 4), "y"},
+                     {acc_out, m * n * 4, "acc_out"}};
+  for (int i = 4; i < 7; ++i) BL_TRY(check_apart(sp[i], sp, i));
+  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, K, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+                              acc_out, static_cast<uint32_t*>(workspace)},
+                   static_cast<cudaStream_t>(stream));
+}
+
+int bitlinear_forward_i8(const int8_t* wq, const float* wscale, int N, int K, const void* x, int x_dtype, int M, void* y,
+                         int y_dtype, int32_t* acc_out, void* workspace, size_t workspace_bytes, void* stream) {
+  BL_TRY(check_dtype(x_dtype, "x_dtype"));
+  BL_TRY(check_i8(N, K, M, y_dtype));
+  if (M == 0) return BL_OK;
+  BL_TRY(check_here(wq, "wq", 16));
+  BL_TRY(check_here(wscale, "wscale", 4));
+  BL_TRY(check_here(x, "x", 16));
+  BL_TRY(check_here(y, "y", 16));
+  BL_TRY(check_here(acc_out, "acc_out", 16, true));
+  BL_TRY(check_here(workspace, "workspace", 256));
+  const FwdLayout l = forward_layout(M, K);
+  if (workspace_bytes < l.total)
+    return fail(BL_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, l.total);
+  const size_t n = static_cast<size_t>(N), m = static_cast<size_t>(M);
+  const Span sp[] = {{wq, n * K, "wq"}, {wscale, n * 4, "wscale"}, {x, m * K * (x_dtype == BL_BF16 ? 2 : 4), "x"},
+                     {workspace, l.total, "workspace"}, {y, m * n * (y_dtype == BL_BF16 ? 2 : 4), "y"},
+                     {acc_out, m * n * 4, "acc_out"}};
+  for (int i = 3; i < 6; ++i) BL_TRY(check_apart(sp[i], sp, i));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
+  float* scale = reinterpret_cast<float*>(ws + l.scale);
+  const int ldq = code_pitch(K);
+  cudaError_t e = bl::launch_act_quant(x, x_dtype == BL_BF16, M, K, ldq, xq, scale, nullptr, s, true);
+  if (e != cudaSuccess) return cuda_fail(e, "act_quant launch");
+  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, ldq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+                              acc_out, static_cast<uint32_t*>(workspace)},
+                   s);
+}
+
 size_t bitlinear_workspace_bytes(int M, int N, int K) {
   (void)N;
   if (M < 0 || K < 0) return 0;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace bl {
 
@@ -190,6 +191,24 @@ size_t ste_scratch_bytes(int M, int N, int K);
 cudaError_t launch_ste_backward(const uint8_t* packed, const float* gamma, int N, int K, const void* dy, const int8_t* xq,
                                 const float* scale, int M, void* dx, bool dx_bf16, float* dw, uint8_t* scratch,
                                 uint32_t* status, cudaStream_t stream);
+
+// The 8-bit product: y = acc / (s[m] * ws[n]) with acc = sum_k xq[m][k] * wq[n][k] in int32.
+struct I8Args {
+  const int8_t* wq;      // [N][K]
+  const float* wscale;   // [N]
+  int N, K, M;
+  const int8_t* xq;      // [M][ldx]
+  int ldx;               // >= K, a multiple of 16
+  const float* scale;    // [M]
+  void* y;               // [M][N]
+  int y_type;            // OutType
+  int32_t* acc_out;      // [M][N] or null
+  uint32_t* status;
+};
+constexpr int kI8MaxK = 131008;       // 128 * 128 * K < 2^31
+constexpr int kI8GemvMaxTokens = 32;
+cudaError_t launch_i8_gemv(const I8Args& a, cudaStream_t stream, bool pdl);  // M <= kI8GemvMaxTokens
+cudaError_t launch_i8_gemm(const I8Args& a, cudaStream_t stream, bool pdl);
 
 // Self-test of the bounded device wait.
 cudaError_t launch_wait_timeout_selftest(uint32_t* status, int limit_us, cudaStream_t stream);

@@ -1,0 +1,237 @@
+"""The 8-bit product with a scale for each token and each output channel, on the GPU.
+
+Accumulators against 64-bit products of the codes, which are exact, bit for
+bit.  Outputs bit for bit against the documented fp32 steps
+fp32(acc) * ((1 / s) * (1 / ws)), done by numpy, and within the bar of their
+roundings of the exact acc / (s ws): both reciprocals, their product, the
+accumulator's conversion and the last product are half a step each, 5 * 2^-24
+(1 + 2^-20), and for bf16 one more of 2^-8.
+"""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import ternary_weight_a8_b200 as tb
+from parity import activations, dev, f32_bits, weights
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _codes(rows, K, seed, full=True):
+    rng = np.random.RandomState(seed)
+    q = rng.randint(-128 if full else -127, 128, size=(rows, K)).astype(np.int8)
+    s = np.exp(rng.uniform(-3, 8, size=rows)).astype(np.float32)
+    return q, s
+
+
+def _exact_acc(q, w):
+    return (q.astype(np.float64) @ w.astype(np.float64).T).astype(np.int64)
+
+
+def _want(acc, s, ws, dtype):
+    f = (np.float32(1) / s)[:, None] * (np.float32(1) / ws)[None, :]
+    y = acc.astype(np.int32).astype(np.float32) * f
+    return torch.from_numpy(y).to(dtype).float().numpy()
+
+
+def _check(y, acc, q, s, w, ws):
+    acc_ref = _exact_acc(q, w)
+    assert np.array_equal(acc.cpu().numpy(), acc_ref)
+    got = y.float().cpu().numpy()
+    assert np.array_equal(f32_bits(got), f32_bits(_want(acc_ref, s, ws, y.dtype)))
+    real = acc_ref / (s.astype(np.float64)[:, None] * ws.astype(np.float64)[None, :])
+    rel = 5 * U * (1 + 2.0 ** -20) + (2.0 ** -8 if y.dtype == torch.bfloat16 else 0.0)
+    assert (np.abs(got - real) <= rel * np.abs(real)).all()
+
+
+SHAPES = [  # M, N, K
+    (1, 1, 64), (1, 17, 64), (2, 5, 192), (1, 6912, 2560), (3, 333, 320), (7, 64, 8640), (8, 100, 128), (9, 1000, 640),
+    (16, 3200, 8640), (17, 16, 2560), (24, 515, 1024), (31, 257, 64), (32, 2560, 6912),
+    (33, 1, 64), (33, 130, 192), (47, 6912, 2560), (64, 63, 8640), (100, 2561, 320), (128, 64, 28672), (128, 10240, 512),
+    (129, 70, 128), (129, 2560, 2560), (200, 20000, 192), (255, 333, 1024), (256, 4096, 64), (300, 7001, 448),
+    (513, 515, 2560), (700, 6912, 320), (1025, 9472, 256),
+]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_parity(M, N, K, dtype):
+    q, s = _codes(M, K, M + K)
+    w, ws = _codes(N, K, N + K)
+    wd, wsd, qd, sd = dev(w), dev(ws), dev(q), dev(s)
+    y, acc = tb.forward_i8_quantized(wd, wsd, qd, sd, out_dtype=dtype, acc_out=True)
+    _check(y, acc, q, s, w, ws)
+    assert torch.equal(tb.forward_i8_quantized(wd, wsd, qd, sd, out_dtype=dtype), y)
+    if M <= 32:  # the other kernel
+        tb.set_path(tb.PATH_GEMM)
+        try:
+            y2, acc2 = tb.forward_i8_quantized(wd, wsd, qd, sd, out_dtype=dtype, acc_out=True)
+            y3 = tb.forward_i8_quantized(wd, wsd, qd, sd, out_dtype=dtype)
+        finally:
+            tb.set_path(tb.PATH_AUTO)
+        assert torch.equal(acc2, acc) and torch.equal(y2, y) and torch.equal(y3, y)
+
+
+@pytest.mark.parametrize("M", [1, 5, 32, 40, 300])
+@pytest.mark.parametrize("K", [64, 2560, 8640])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantises_activations(M, K, dtype):
+    """forward_i8 = quant_act, then the product on its codes; the weights through quant_weights_i8."""
+    N = 210
+    W = weights(N, K, seed=K)
+    x, xf = activations(M, K, seed=M + K, dtype=dtype)
+    wq_ref, ws_ref, _ = oracle.quant_act(W)
+    q_ref, s_ref, _ = oracle.quant_act(xf)
+    wq, ws = tb.quant_weights_i8(dev(W))
+    assert np.array_equal(wq.cpu().numpy(), wq_ref) and np.array_equal(f32_bits(ws.cpu().numpy()), f32_bits(ws_ref))
+    y, acc = tb.forward_i8(wq, ws, x, out_dtype=torch.float32, acc_out=True)
+    _check(y, acc, q_ref, s_ref, wq_ref, ws_ref)
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_extreme_sums(M):
+    """The longest sums of the largest codes: -128 * -128 * K stays inside int32."""
+    K, N = 131008, 3
+    q = np.full((M, K), -128, np.int8)
+    w = np.full((N, K), -128, np.int8)
+    w[1] = 127
+    s, ws = np.full(M, 2.0, np.float32), np.full(N, 4.0, np.float32)
+    y, acc = tb.forward_i8_quantized(dev(w), dev(ws), dev(q), dev(s), out_dtype=torch.float32, acc_out=True)
+    _check(y, acc, q, s, w, ws)
+    big = torch.zeros((1, 131072), dtype=torch.int8, device="cuda")
+    with pytest.raises(tb.BitLinearError) as e:
+        tb.forward_i8_quantized(big, dev(ws[:1]), big, dev(s[:1]))
+    assert e.value.code == tb.BL_ERR_UNSUPPORTED_SHAPE
+
+
+@pytest.mark.parametrize("M", [2, 50])
+def test_zero_tokens_and_channels(M):
+    """A zero token or channel gives zeros; its scale is 127 / 1e-5."""
+    W = weights(70, 256, seed=1)
+    W[3] = 0
+    x, xf = activations(M, 256, seed=2, dtype="f32")
+    x[1] = 0
+    wq, ws = tb.quant_weights_i8(dev(W))
+    y = tb.forward_i8(wq, ws, x, out_dtype=torch.float32)
+    assert not y[1].any() and not y[:, 3].any() and torch.isfinite(y).all() and y[0].any()
+    assert tb.forward_i8(wq, ws, x[:0]).shape == (0, 70)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 333, 320), (20, 64, 128), (40, 100, 8640), (150, 4001, 192), (300, 9000, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_no_writes_outside_outputs(M, N, K, dtype):
+    pad, canary = 4096, 0x5A
+    q, s = _codes(M, K, 1)
+    w, ws = _codes(N, K, 2)
+    size = M * N * (2 if dtype == torch.bfloat16 else 4)
+    ybuf = torch.full((2 * pad + size,), canary, dtype=torch.uint8, device="cuda")
+    abuf = torch.full((2 * pad + M * N * 4,), canary, dtype=torch.uint8, device="cuda")
+    wbuf = torch.full((256 + pad,), canary, dtype=torch.uint8, device="cuda")
+    wbuf[:256] = 0
+    y, acc = ybuf[pad:pad + size].view(dtype).view(M, N), abuf[pad:pad + M * N * 4].view(torch.int32).view(M, N)
+    tb.forward_i8_quantized(dev(w), dev(ws), dev(q), dev(s), y=y, acc_out=acc, workspace=wbuf[:256])
+    _check(y, acc, q, s, w, ws)
+    for buf in (ybuf[:pad], ybuf[-pad:], abuf[:pad], abuf[-pad:], wbuf[256:]):
+        assert (buf == canary).all()
+    assert tb.device_status(wbuf[:256]) == tb.BL_OK
+
+
+@pytest.mark.parametrize("M", [1, 48, 512])
+def test_weights_written_just_before(M):
+    """Weights that the kernel just before the call wrote: every call sees them whole."""
+    N, K = 4096, 2560
+    x, _ = activations(M, K, seed=1, dtype="bf16")
+    xq, s, _ = tb.quant_act(x)
+    sets = [dev(weights(N, K, seed=10 + i)) for i in range(2)]
+    want = []
+    for W in sets:
+        wq, ws = tb.quant_weights_i8(W)
+        torch.cuda.synchronize()
+        want.append(tb.forward_i8_quantized(wq, ws, xq, s))
+    torch.cuda.synchronize()
+    wq, ws = torch.empty((N, K), dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    got = []
+    for i in range(30):
+        tb.quant_weights_i8(sets[i % 2], wq, ws)
+        got.append((tb.forward_i8_quantized if i % 4 < 2 else tb.forward_i8)(wq, ws, *((xq, s) if i % 4 < 2 else (x,))))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2]), i
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_streams_threads_and_graphs(M):
+    N, K = 3001, 2560
+    wq, ws = tb.quant_weights_i8(dev(weights(N, K, seed=1)))
+    xs = [activations(M, K, seed=20 + k, dtype="bf16")[0] for k in range(2)]
+    want = [tb.forward_i8(wq, ws, x) for x in xs]
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = tb.forward_i8(wq, ws, xs[0], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want[0])
+    bad = []
+
+    def work(k):
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                y = tb.forward_i8(wq, ws, xs[k])
+                side.synchronize()
+                if not torch.equal(y, want[k]):
+                    bad.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad
+    graphs = []
+    for k in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y = tb.forward_i8(wq, ws, xs[k])
+        graphs.append((graph, y))
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graphs[0][0].replay()
+        with torch.cuda.stream(other):
+            graphs[1][0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1], want[0]) and torch.equal(graphs[1][1], want[1])
+
+
+def test_refusals():
+    w, ws = torch.zeros((64, 128), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    q, s = torch.zeros((4, 128), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    x = torch.zeros((4, 128), device="cuda")
+    for bad in (lambda: tb.forward_i8(w, ws, x[:, :64].contiguous()), lambda: tb.forward_i8(w.float(), ws, x),
+                lambda: tb.forward_i8(w, ws[:3], x), lambda: tb.forward_i8(w, ws.double(), x),
+                lambda: tb.forward_i8(w, ws, x.half()), lambda: tb.forward_i8(w, ws, x, out_dtype=torch.float16),
+                lambda: tb.forward_i8(w.cpu(), ws, x), lambda: tb.forward_i8(w, ws, x.cpu()),
+                lambda: tb.forward_i8(w.t(), ws, x), lambda: tb.forward_i8(w, ws, x, y=torch.empty((4, 65), device="cuda")),
+                lambda: tb.forward_i8_quantized(w, ws, x, s), lambda: tb.forward_i8_quantized(w, ws, q, s[:2]),
+                lambda: tb.forward_i8_quantized(w, ws, q, s, acc_out=torch.empty((4, 64), device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    odd = torch.zeros((4, 96), dtype=torch.int8, device="cuda")
+    many = torch.zeros((33, 128), dtype=torch.int8, device="cuda")
+    buf = torch.zeros(4 * 128 + 64, dtype=torch.int8, device="cuda")
+    for bad, code in ((lambda: tb.forward_i8_quantized(odd, torch.ones(4, device="cuda"), odd, s), tb.BL_ERR_UNSUPPORTED_SHAPE),
+                      (lambda: tb.forward_i8(w, ws, x, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")),
+                       tb.BL_ERR_WORKSPACE_TOO_SMALL),
+                      (lambda: tb.forward_i8_quantized(w, ws, buf[1:513].view(4, 128), s), tb.BL_ERR_MISALIGNED),
+                      (lambda: tb.forward_i8_quantized(w, ws, q, s, y=w.view(-1)[:1024].view(torch.float32).view(4, 64)),
+                       tb.BL_ERR_INVALID_ARG)):
+        with pytest.raises(tb.BitLinearError) as e:
+            bad()
+        assert e.value.code == code
+    tb.set_path(tb.PATH_GEMV)
+    try:
+        with pytest.raises(tb.BitLinearError) as e:
+            tb.forward_i8_quantized(w, ws, many, torch.ones(33, device="cuda"))
+        assert e.value.code == tb.BL_ERR_UNSUPPORTED_SHAPE
+    finally:
+        tb.set_path(tb.PATH_AUTO)
