@@ -164,7 +164,7 @@ size_t bitlinear_add_rmsnorm_backward_workspace_bytes(int M, int K, int z_dtype)
  * gd = dnorm * gain:
  *   dz    = r * (gd - n * mean_k(gd * n)) + dz_in
  *   dgain = sum over tokens of dnorm * n
- * in fp32 (the squares of z in double); dz is rounded once.
+ * in fp32; dz is rounded once.
  *   z       device [M][K] of z_dtype: the forward's z.
  *   dnorm   device [M][K] of dnorm_dtype (BL_F32 or BL_BF16): the gradient of
  *           the normalised activations.

@@ -26,74 +26,179 @@ namespace bl {
 
 namespace {
 
-// 16 bytes of activations: 8 bf16 or 4 fp32.
+// 16 bytes of activations: 8 bf16 or 4 fp32, handled as pairs of fp32 in the
+// packed two-wide fp32 instructions (each half rounds as the scalar one does).
 template <typename T>
 constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+constexpr int kPairs = kPer<T> / 2;
 
-__device__ __forceinline__ uint32_t bf16_bits_rn(float v) {
-  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v)));
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ f32x2 pair_of_bf16(uint32_t w) {  // exact
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t bf16_of_pair(f32x2 v) {
+  float lo, hi;
+  split2(v, lo, hi);
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack16(const uint4& w, float (&f)[kPer<T>]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      f[2 * i] = __uint_as_float(u[i] << 16);  // bf16 -> fp32 is exact
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    } else {
-      f[i] = __uint_as_float(u[i]);
-    }
+__device__ __forceinline__ void to_pairs(const uint4& w, f32x2 (&p)[kPairs<T>]) {
+  if constexpr (sizeof(T) == 2) {
+    p[0] = pair_of_bf16(w.x);
+    p[1] = pair_of_bf16(w.y);
+    p[2] = pair_of_bf16(w.z);
+    p[3] = pair_of_bf16(w.w);
+  } else {
+    p[0] = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
+    p[1] = pack2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
 }
 
+// The pairs rounded to T.
 template <typename T>
-__device__ __forceinline__ uint4 pack16(const float (&f)[kPer<T>]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2) {
-      u[i] = bf16_bits_rn(f[2 * i]) | (bf16_bits_rn(f[2 * i + 1]) << 16);
-    } else {
-      u[i] = __float_as_uint(f[i]);
-    }
+__device__ __forceinline__ uint4 from_pairs(const f32x2 (&p)[kPairs<T>]) {
+  if constexpr (sizeof(T) == 2) {
+    return make_uint4(bf16_of_pair(p[0]), bf16_of_pair(p[1]), bf16_of_pair(p[2]), bf16_of_pair(p[3]));
+  } else {
+    float f[4];
+    split2(p[0], f[0], f[1]);
+    split2(p[1], f[2], f[3]);
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// N consecutive fp32 values (the gains of a chunk, 16-byte aligned).
-template <int N>
-__device__ __forceinline__ void load_f32(const float* p, float (&f)[N]) {
+// a + b in T.  For bf16 one rounding of the exact sum equals fp32's sum
+// rounded once more: a sum that fp32 cannot hold has its smaller term below
+// 2^-15 of the larger, far under half a bf16 step.
+template <typename T>
+__device__ __forceinline__ uint4 sum16(const uint4& a, const uint4& b) {
+  if constexpr (sizeof(T) == 2) {
+    auto add = [](uint32_t u, uint32_t v) {
+      const __nv_bfloat162 h = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                          *reinterpret_cast<const __nv_bfloat162*>(&v));
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    return make_uint4(add(a.x, b.x), add(a.y, b.y), add(a.z, b.z), add(a.w, b.w));
+  } else {
+    f32x2 p[2], q[2];
+    to_pairs<float>(a, p);
+    to_pairs<float>(b, q);
+    p[0] = add2(p[0], q[0]);
+    p[1] = add2(p[1], q[1]);
+    return from_pairs<float>(p);
+  }
+}
+
+// The largest |value| of chunks, as its bits (of T; two 16-bit maxima for
+// bf16): the order of the bits is that of the values, infinity above every
+// number and NaN above infinity.
+template <typename T>
+__device__ __forceinline__ uint32_t absmax16(uint32_t m, const uint4& w) {
+  if constexpr (sizeof(T) == 2) {
+    m = __vmaxu2(m, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu));
+    return __vmaxu2(m, __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  } else {
+    m = max(m, max(w.x & 0x7fffffffu, w.y & 0x7fffffffu));
+    return max(m, max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
+  }
+}
+// As fp32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t absmax_bits(uint32_t m) {
+  if constexpr (sizeof(T) == 2) return max(m & 0xffffu, m >> 16) << 16;
+  return m;
+}
+
+// N fp32 values (the gains of a chunk, 16-byte aligned).
+template <int P2>
+__device__ __forceinline__ void load_pairs(const float* p, f32x2 (&f)[P2]) {
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
+  for (int i = 0; i < P2 / 2; ++i) {
     const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
-    f[4 * i] = q.x;
-    f[4 * i + 1] = q.y;
-    f[4 * i + 2] = q.z;
-    f[4 * i + 3] = q.w;
+    f[2 * i] = pack2(q.x, q.y);
+    f[2 * i + 1] = pack2(q.z, q.w);
   }
 }
 
-// Codes of N values (4 or 8), stored together; returns their sum.
-template <int N>
-__device__ __forceinline__ int store_codes(const float (&v)[N], float s, int8_t* dst) {
-  uint32_t w[N / 4];
-  int sum = 0;
+// Codes of a chunk of finite values, stored together; returns their sum.
+// |v * s| <= 127 (1 + 2^-23), so no code needs clamping, and adding 1.5 * 2^23
+// to the rounded product leaves rint of it (ties to even) in the sum's low bits.
+// The sums are scalar: a packed sum of a packed product came out fused
+// (-2.125 * 29.882353, -63.5 once rounded, gave -63), .rn on both or not.
+template <typename T>
+__device__ __forceinline__ int store_codes(const uint4& v, f32x2 s2, int8_t* dst) {
+  constexpr float kMagic = 12582912.0f;
+  f32x2 p[kPairs<T>];
+  to_pairs<T>(v, p);
+  uint32_t w[kPairs<T> / 2];
 #pragma unroll
-  for (int b = 0; b < N / 4; ++b) {
-    int q[4];
+  for (int b = 0; b < kPairs<T> / 2; ++b) {
+    float f[4];
+    split2(mul2(p[2 * b], s2), f[0], f[1]);
+    split2(mul2(p[2 * b + 1], s2), f[2], f[3]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = min(max(__float2int_rn(__fmul_rn(v[4 * b + e], s)), -128), 127);
-    const uint32_t lo = __byte_perm(static_cast<uint32_t>(q[0]), static_cast<uint32_t>(q[1]), 0x5140);
-    const uint32_t hi = __byte_perm(static_cast<uint32_t>(q[2]), static_cast<uint32_t>(q[3]), 0x5140);
+    for (int e = 0; e < 4; ++e) f[e] = __fadd_rn(f[e], kMagic);
+    const uint32_t lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040);
     w[b] = __byte_perm(lo, hi, 0x5410);
-    sum = __dp4a(static_cast<int>(w[b]), 0x01010101, sum);
   }
-  if constexpr (N == 8) {
+  int sum = 0;
+  if constexpr (sizeof(T) == 2) {
+    sum = __dp4a(static_cast<int>(w[1]), 0x01010101, __dp4a(static_cast<int>(w[0]), 0x01010101, 0));
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   } else {
+    sum = __dp4a(static_cast<int>(w[0]), 0x01010101, 0);
     *reinterpret_cast<uint32_t*>(dst) = w[0];
+  }
+  return sum;
+}
+
+// The same for a token with infinities or NaN: NaN products (NaN * s, and
+// infinity * 0, since an infinity makes s zero) give code 0.
+template <typename T>
+__device__ __forceinline__ int store_codes_any(const uint4& v, float s, int8_t* dst) {
+  f32x2 p[kPairs<T>];
+  to_pairs<T>(v, p);
+  int sum = 0;
+#pragma unroll
+  for (int b = 0; b < kPairs<T>; ++b) {
+    float f[2];
+    split2(p[b], f[0], f[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int q = min(max(__float2int_rn(__fmul_rn(f[e], s)), -128), 127);
+      dst[2 * b + e] = static_cast<int8_t>(q);
+      sum += q;
+    }
   }
   return sum;
 }
@@ -113,6 +218,7 @@ __device__ __forceinline__ V warp_reduce(V v, Op op) {
 // groups as fit in 256 threads, or one.
 constexpr int kMaxGroupWarps = 16;
 constexpr int kNormThreads = 256;
+constexpr int kMaxRowBytes = 224 * 1024;  // of a long token in shared memory
 
 // The value of every warp of the token's group, combined in warp order (the
 // same in every thread).  `slot`: this group's W values in shared memory.  The
@@ -128,7 +234,22 @@ __device__ __forceinline__ V group_reduce(V v, Op op, V* slot, int W, int wig, i
   return r;
 }
 
-__device__ __forceinline__ float rstd_of(double ss, int K, float eps) {
+// fp32(1 / sqrt(ss / K + eps)) exactly as the divisions and the square root
+// in double give it.  Those cost hundreds of instructions, and every thread
+// needs the value, so it is first taken from rsqrtf and two steps of Newton's
+// method in double (y += y / 2 (1 - x y^2)), which is within 2^-50; only when
+// that lies within 2^-44 of a border between two fp32 values, or outside the
+// range where fp32's rsqrtf starts well, are the divisions done.
+__device__ __forceinline__ float rstd_of(double ss, int K, double inv_k, float eps) {
+  const double x = __fma_rn(ss, inv_k, static_cast<double>(eps));
+  if (x > 1e-30 && x < 1e30) {
+    double y = static_cast<double>(rsqrtf(static_cast<float>(x)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = __fma_rn(0.5 * y, __fma_rn(-x * y, y, 1.0), y);
+    // The 29 bits that fp32 drops, from the middle between two values.
+    const int off = static_cast<int>(__double_as_longlong(y) & 0x1fffffffll) - 0x10000000;
+    if (off > 256 || off < -256) return __double2float_rn(y);
+  }
   const double ms = __ddiv_rn(ss, static_cast<double>(K));
   return __double2float_rn(__ddiv_rn(1.0, __dsqrt_rn(__dadd_rn(ms, static_cast<double>(eps)))));
 }
@@ -144,16 +265,22 @@ struct AddNormParams {
   float* scale;
   int32_t* rowsum;  // or null
   int M, K;
+  double inv_k;
 };
 
-// C: 16-byte chunks of a token per thread, held in registers from the sum to
+// kFull: the token's chunks are exactly the threads' (no bounds to test, and
+// the chunks' instructions interleave).  C: 16-byte chunks of a token per thread, held in registers from the sum to
 // the codes (z's chunk is overwritten by v's).  C = 0: the token is longer
-// than the registers hold; z is read back (each thread its own chunks) for
-// the absmax and again for the codes.
-template <typename T, int C>
-__global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(const AddNormParams P, int W) {
+// than the registers hold, and its chunks wait in shared memory (`staged`), or,
+// longer than that too, z is read back for the absmax and again for the
+// codes; either way each thread reads only what it wrote.
+template <typename T, int C, bool kFull>
+__global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
+                                                                                         int staged) {
+  extern __shared__ uint4 row_buf[];
   constexpr int N = kPer<T>;
   __shared__ double red_d[kMaxGroupWarps];
+  __shared__ uint32_t red_u[kMaxGroupWarps];
   __shared__ float red_f[kMaxGroupWarps];
   __shared__ int red_i[kMaxGroupWarps];
   griddep_launch_dependents();
@@ -172,41 +299,43 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(const AddNormPar
   uint4* nr = P.x_norm ? reinterpret_cast<uint4*>(static_cast<T*>(P.x_norm) + row) : nullptr;
   int8_t* qr = P.xq + row;
 
-  auto sum_chunk = [&](const uint4& a, const uint4& b, double& ss) {
-    float fa[N], fb[N];
-    unpack16<T>(a, fa);
-    unpack16<T>(b, fb);
+  // Squares in double, in two chains.
+  double ss0 = 0.0, ss1 = 0.0;
+  auto square = [&](const uint4& zc) {
+    f32x2 p[kPairs<T>];
+    to_pairs<T>(zc, p);
 #pragma unroll
-    for (int e = 0; e < N; ++e) fa[e] = round_to<T>(__fadd_rn(fa[e], fb[e]));
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const double v = static_cast<double>(fa[e]);
-      ss = __fma_rn(v, v, ss);
+    for (int e = 0; e < kPairs<T>; ++e) {
+      float lo, hi;
+      split2(p[e], lo, hi);
+      const double dl = static_cast<double>(lo), dh = static_cast<double>(hi);
+      ss0 = __fma_rn(dl, dl, ss0);
+      ss1 = __fma_rn(dh, dh, ss1);
     }
-    return pack16<T>(fa);
   };
-  float r = 0.0f;
-  auto norm_chunk = [&](const uint4& zc, int c, float (&v)[N]) {
-    unpack16<T>(zc, v);
-    float g[N];
-    if (P.gain) load_f32<N>(P.gain + static_cast<size_t>(c) * N, g);
+  f32x2 r2 = 0;
+  auto norm_chunk = [&](const uint4& zc, int c) {
+    f32x2 p[kPairs<T>];
+    to_pairs<T>(zc, p);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      float t = __fmul_rn(v[e], r);
-      if (P.gain) t = __fmul_rn(t, g[e]);
-      v[e] = round_to<T>(t);
+    for (int e = 0; e < kPairs<T>; ++e) p[e] = mul2(p[e], r2);
+    if (P.gain) {
+      f32x2 g[kPairs<T>];
+      load_pairs(P.gain + static_cast<size_t>(c) * N, g);
+#pragma unroll
+      for (int e = 0; e < kPairs<T>; ++e) p[e] = mul2(p[e], g[e]);
     }
+    return from_pairs<T>(p);
   };
 
   constexpr int CR = C > 0 ? C : 1;
   uint4 keep[CR];
-  double ss = 0.0;
   if constexpr (C > 0) {
     uint4 other[CR];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
-      if (c < chunks) {
+      if (kFull || c < chunks) {
         keep[i] = __ldcg(xr + c);
         other[i] = __ldcg(rr + c);
       }
@@ -214,65 +343,113 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(const AddNormPar
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
-      if (c < chunks) {
-        keep[i] = sum_chunk(keep[i], other[i], ss);
+      if (kFull || c < chunks) {
+        keep[i] = sum16<T>(keep[i], other[i]);
         zr[c] = keep[i];
+        square(keep[i]);
       }
     }
   } else {
-    for (int c = tid; c < chunks; c += step) zr[c] = sum_chunk(__ldcg(xr + c), __ldcg(rr + c), ss);
-  }
-  ss = group_reduce(ss, [](double a, double b) { return __dadd_rn(a, b); }, red_d + group * W, W, wig, lane, bar);
-  r = rstd_of(ss, P.K, P.eps);
-
-  float amax = 0.0f;
-  auto amax_of = [&](const float (&v)[N]) {
+    for (int c0 = tid; c0 < chunks; c0 += 4 * step) {
+      uint4 a[4], b[4];
 #pragma unroll
-    for (int e = 0; e < N; ++e) amax = fmaxf(amax, fabsf(v[e]));
-  };
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i * step < chunks) {
+          a[i] = __ldcg(xr + c0 + i * step);
+          b[i] = __ldcg(rr + c0 + i * step);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * step;
+        if (c < chunks) {
+          const uint4 zc = sum16<T>(a[i], b[i]);
+          zr[c] = zc;
+          if (staged) row_buf[c] = zc;
+          square(zc);
+        }
+      }
+    }
+  }
+  const double ss = group_reduce(__dadd_rn(ss0, ss1), [](double a, double b) { return __dadd_rn(a, b); },
+                                 red_d + group * W, W, wig, lane, bar);
+  const float r = rstd_of(ss, P.K, P.inv_k, P.eps);
+  r2 = pack2(r, r);
+
+  uint32_t top = 0;
   if constexpr (C > 0) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
-      if (c < chunks) {
-        float v[N];
-        norm_chunk(keep[i], c, v);
-        amax_of(v);
-        keep[i] = pack16<T>(v);  // exact: v is rounded to T
+      if (kFull || c < chunks) {
+        keep[i] = norm_chunk(keep[i], c);
+        top = absmax16<T>(top, keep[i]);
         if (nr) nr[c] = keep[i];
       }
     }
   } else {
     for (int c = tid; c < chunks; c += step) {
-      float v[N];
-      norm_chunk(zr[c], c, v);
-      amax_of(v);
+      const uint4 v = norm_chunk(staged ? row_buf[c] : zr[c], c);
+      top = absmax16<T>(top, v);
+      if (staged) row_buf[c] = v;
     }
   }
-  amax = group_reduce(amax, [](float a, float b) { return fmaxf(a, b); }, red_f + group * W, W, wig, lane, bar);
-  const float s = __fdiv_rn(127.0f, fmaxf(amax, 1e-5f));
-
-  int sum = 0;
-  if constexpr (C > 0) {
+  top = __reduce_max_sync(0xffffffffu, absmax_bits<T>(top));
+  if (W > 1) {
+    if (lane == 0) red_u[group * W + wig] = top;
+    group_sync(bar, 32 * W);
+    for (int i = 0; i < W; ++i) top = max(top, red_u[group * W + i]);
+  }
+  float amax = __uint_as_float(top);
+  const bool finite = top < 0x7f800000u;  // the same in the whole group
+  // fn(values, chunk) over the normalised chunks.
+  auto for_each = [&](auto&& fn) {
+    if constexpr (C > 0) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = tid + i * step;
-      if (c < chunks) {
-        float v[N];
-        unpack16<T>(keep[i], v);
-        sum += store_codes<N>(v, s, qr + static_cast<size_t>(c) * N);
+      for (int i = 0; i < C; ++i) {
+        const int c = tid + i * step;
+        if (kFull || c < chunks) fn(keep[i], c);
       }
+    } else {
+      for (int c = tid; c < chunks; c += step) fn(staged ? row_buf[c] : norm_chunk(zr[c], c), c);
     }
+  };
+  int sum = 0;
+  float s;
+  if (finite) {
+    s = __fdiv_rn(127.0f, fmaxf(amax, 1e-5f));
+    const f32x2 s2 = pack2(s, s);
+    for_each([&](const uint4& v, int c) {
+      if (C == 0 && nr) nr[c] = v;
+      sum += store_codes<T>(v, s2, qr + static_cast<size_t>(c) * N);
+    });
   } else {
-    for (int c = tid; c < chunks; c += step) {
-      float v[N];
-      norm_chunk(zr[c], c, v);
-      if (nr) nr[c] = pack16<T>(v);
-      sum += store_codes<N>(v, s, qr + static_cast<size_t>(c) * N);
-    }
+    // Infinities or NaN: the largest |value| that is a number or an infinity.
+    amax = 0.0f;
+    for_each([&](const uint4& v, int) {
+      f32x2 p[kPairs<T>];
+      to_pairs<T>(v, p);
+#pragma unroll
+      for (int e = 0; e < kPairs<T>; ++e) {
+        float lo, hi;
+        split2(p[e], lo, hi);
+        amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
+      }
+    });
+    amax = group_reduce(amax, [](float a, float b) { return fmaxf(a, b); }, red_f + group * W, W, wig, lane, bar);
+    s = __fdiv_rn(127.0f, fmaxf(amax, 1e-5f));
+    for_each([&](const uint4& v, int c) {
+      if (C == 0 && nr) nr[c] = v;
+      sum += store_codes_any<T>(v, s, qr + static_cast<size_t>(c) * N);
+    });
   }
   if (P.rowsum) {
-    sum = group_reduce(sum, [](int a, int b) { return a + b; }, red_i + group * W, W, wig, lane, bar);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (W > 1) {
+      if (lane == 0) red_i[group * W + wig] = sum;
+      group_sync(bar, 32 * W);
+      if (tid == 0)
+        for (int i = 1; i < W; ++i) sum += red_i[group * W + i];
+    }
     if (tid == 0) P.rowsum[m] = sum;
   }
   if (tid == 0) P.scale[m] = s;
@@ -281,29 +458,47 @@ __global__ void __launch_bounds__(512) add_rmsnorm_quant_kernel(const AddNormPar
 template <typename T>
 cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stream, bool pdl) {
   const int chunks = P.K / kPer<T>;
-  // Chunks per thread n and warps per token W: eight chunks per thread (the
-  // fewest warps to join) while the tokens give every SM 16 warps, else fewer
-  // chunks and more warps, as far as a block goes.
+  // Chunks per thread n and warps per token W: four chunks per thread (the
+  // most that leave 32 warps to an SM) while the tokens give every SM 16
+  // warps, else fewer chunks and more warps, as far as a block goes.
   int W = 0, n = 0;
-  for (int c = 8; c >= 1; c /= 2) {
-    const int w = (chunks + 32 * c - 1) / (32 * c);
+  for (int c = 4; c >= 1; c /= 2) {
+    int w = (chunks + 32 * c - 1) / (32 * c);
+    if (w > 8) w = (w + 3) / 4 * 4;  // an even share of an SM's four schedulers and their registers
     if (w > kMaxGroupWarps) break;
     W = w;
     n = (chunks + 32 * w - 1) / (32 * w);
     if (static_cast<long long>(P.M) * w >= 16LL * num_sms()) break;
   }
-  if (W == 0) {  // longer than 16 warps hold
-    W = kMaxGroupWarps;
-    n = 9;
+  if (W == 0) {
+    // Longer than 16 warps hold.  Up to nine chunks a thread, eight warps leave
+    // room for more tokens on an SM (1021 fp32 tokens of 8640: 26.8 us, 33.0
+    // with 16 warps); longer tokens want all 16 (512 bf16 tokens of 28672:
+    // 28.2 us, 36.0 with 8).
+    W = chunks <= 9 * 32 * 8 ? 8 : kMaxGroupWarps;
+    n = 5;
   }
   const int groups = W > kNormThreads / 32 ? 1 : kNormThreads / 32 / W;
   const int threads = 32 * W * groups;
   const dim3 grid((P.M + groups - 1) / groups);
-  if (n <= 1) return launch(add_rmsnorm_quant_kernel<T, 1>, grid, dim3(threads), 0, stream, pdl, P, W);
-  if (n <= 2) return launch(add_rmsnorm_quant_kernel<T, 2>, grid, dim3(threads), 0, stream, pdl, P, W);
-  if (n <= 4) return launch(add_rmsnorm_quant_kernel<T, 4>, grid, dim3(threads), 0, stream, pdl, P, W);
-  if (n <= 8) return launch(add_rmsnorm_quant_kernel<T, 8>, grid, dim3(threads), 0, stream, pdl, P, W);
-  return launch(add_rmsnorm_quant_kernel<T, 0>, grid, dim3(threads), 0, stream, pdl, P, W);
+  const int held = n <= 2 ? n : 4;
+  const bool full = chunks == held * 32 * W;  // every thread holds as many chunks as it has room for
+  if (n <= 1) return full ? launch(add_rmsnorm_quant_kernel<T, 1, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
+                : launch(add_rmsnorm_quant_kernel<T, 1, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
+  if (n <= 2) return full ? launch(add_rmsnorm_quant_kernel<T, 2, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
+                : launch(add_rmsnorm_quant_kernel<T, 2, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
+  if (n <= 4) return full ? launch(add_rmsnorm_quant_kernel<T, 4, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
+                : launch(add_rmsnorm_quant_kernel<T, 4, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
+  const size_t row = static_cast<size_t>(P.K) * sizeof(T);
+  const bool staged = row <= kMaxRowBytes;
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMaxRowBytes);
+  });
+  if (e != cudaSuccess) return e;
+  return launch(add_rmsnorm_quant_kernel<T, 0, false>, grid, dim3(threads), staged ? row : 0, stream, pdl, P, W,
+                staged ? 1 : 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -316,57 +511,107 @@ struct AddNormBackParams {
   const void* dz_in;   // or null
   float eps;
   void* dz;            // may be dz_in
-  float* part;         // [rows][K] sums of dv * n over each group's tokens, or null
+  float* part;         // [rows][K] sums of dv * n over each block's tokens, or null
   float* rstd;         // [M] (long tokens only)
   int M, K;
+  double inv_k;
+  float inv_kf;
 };
 
-// N gradient values of type TD at element offset `at` (16-byte aligned for N
-// values of TD, or 8 bytes for 4 bf16 values).
+// N gradient values of type TD: 8, 16 or 32 bytes.
 template <typename TD, int N>
 struct GradChunk {
-  uint4 w[N * sizeof(TD) > 16 ? 2 : 1];
+  static constexpr int kBytes = N * static_cast<int>(sizeof(TD));
+  uint4 w[kBytes > 16 ? 2 : 1];
   __device__ __forceinline__ void load(const TD* p) {
-    if constexpr (N * sizeof(TD) == 8) {
+    if constexpr (kBytes == 8) {
       const uint2 h = __ldcg(reinterpret_cast<const uint2*>(p));
       w[0] = make_uint4(h.x, h.y, 0, 0);
     } else {
 #pragma unroll
-      for (int i = 0; i < static_cast<int>(N * sizeof(TD) / 16); ++i)
-        w[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+      for (int i = 0; i < kBytes / 16; ++i) w[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[N]) const {
+  __device__ __forceinline__ void get(f32x2 (&f)[N / 2]) const {
     if constexpr (sizeof(TD) == 2) {
-      float t[8];
-      unpack16<__nv_bfloat16>(w[0], t);
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = t[e];
+      for (int i = 0; i < N / 2; ++i) f[i] = pair_of_bf16(u[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < N / 4; ++i) {
-        float t[4];
-        unpack16<float>(w[i], t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 * i + e] = t[e];
+        f32x2 t[2];
+        to_pairs<float>(w[i], t);
+        f[2 * i] = t[0];
+        f[2 * i + 1] = t[1];
       }
     }
   }
 };
 
-struct SumPair {
-  double ss;
-  float dot;
+// A thread's own pieces of 16 (or 8) bytes on their way through shared memory.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  }
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// The ring of the backward's z and dv: for every stage and chunk, a piece of
+// each thread after the other.  Three stages: a token's output, the next
+// one's sums and the one after on its way.
+template <typename T, typename TD>
+struct BackRing {
+  static constexpr int kZ = 16, kD = kPer<T> * static_cast<int>(sizeof(TD)), kChunk = kZ + kD;
+  static constexpr int kStages = 3;
+  static constexpr int bytes(int threads, int chunks) { return kStages * chunks * threads * kChunk; }
 };
 
+template <int P2>
+__device__ __forceinline__ void store_pairs(float* p, const f32x2 (&v)[P2]) {
+#pragma unroll
+  for (int i = 0; i < P2 / 2; ++i) {
+    float f[4];
+    split2(v[2 * i], f[0], f[1]);
+    split2(v[2 * i + 1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[i] = make_float4(f[0], f[1], f[2], f[3]);
+  }
+}
+
+// Sums of z^2 outside this range are taken again in double (fp32 squares
+// overflow above 2^128 and lose bits below 2^-126).
+constexpr float kSquaresLow = 1e-25f, kSquaresHigh = 1e37f;
+
+// The two sums of a pair over the warp, in one butterfly.
+__device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = add2(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 // A group of W warps takes tokens group0, group0 + groups_total, ...; a
-// thread owns the same C chunks of every token, so the gain's gradient is
-// summed in its registers and written once per group.  The next token's z
-// and dv are requested before the current token's reduction.
-template <typename T, typename TD, int C, bool kGain>
-__global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(const AddNormBackParams P, int W) {
-  constexpr int N = kPer<T>;
-  __shared__ SumPair red[2][kMaxGroupWarps];
+// thread owns the same C chunks of every token (kFull: all of them exist), so the gain's gradient is
+// summed in its registers and written once per block.  The two sums over a
+// token run as one pair of fp32 (trees of at most 26 steps): at 16 warps a
+// token, sums and 1 / rms in double were half of the kernel's instructions.
+// z and dv of the next tokens are under way in shared memory, where a thread
+// reads only what it copied itself, so no barrier guards them; a token's sums
+// are taken while the token before is written, so that the reduction's chain
+// of shuffles and its barrier wait for nobody.
+template <typename T, typename TD, int C, bool kGain, bool kFull>
+__global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 1) add_rmsnorm_backward_kernel(const AddNormBackParams P, int W) {
+  constexpr int N = kPer<T>, NP = kPairs<T>;
+  using R = BackRing<T, TD>;
+  extern __shared__ uint4 ring[];
+  __shared__ f32x2 red[2][kMaxGroupWarps];
+  __shared__ double red_d[kMaxGroupWarps];
   griddep_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -375,123 +620,196 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(const AddNorm
   const int tid = wig * 32 + lane, step = 32 * W, chunks = P.K / N, bar = 1 + group;
   griddep_wait();
 
-  float acc[kGain ? C : 1][N];
+  // The gains and the sums of their gradient stay in registers: reading 4
+  // bytes of gain for every 2 of z, twice a token, kept the kernel waiting.
+  f32x2 acc[kGain ? C : 1][NP], gains[kGain ? C : 1][NP];
 #pragma unroll
-  for (int i = 0; i < (kGain ? C : 1); ++i)
+  for (int i = 0; i < (kGain ? C : 1); ++i) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[i][e] = 0.0f;
+    for (int e = 0; e < NP; ++e) acc[i][e] = 0;
+    if constexpr (kGain) {
+      const int c = tid + i * step;
+      if (kFull || c < chunks) load_pairs(P.gain + static_cast<size_t>(c) * N, gains[i]);
+    }
+  }
 
-  uint4 zc[C];
-  GradChunk<TD, N> dc[C];
-  auto fetch = [&](int m) {
-    const size_t row = static_cast<size_t>(m) * P.K;
+  // Stage s, chunk i: this thread's z, and behind every thread's z its dv (32
+  // bytes as two pieces apart, so that the threads' pieces stay adjacent).
+  const int threads = blockDim.x;
+  uint8_t* const mine = reinterpret_cast<uint8_t*>(ring);
+  auto z_at = [&](int s, int i) { return mine + (s * C + i) * threads * R::kChunk + threadIdx.x * 16; };
+  auto d_at = [&](int s, int i, int j) {
+    return mine + (s * C + i) * threads * R::kChunk + threads * (16 + 16 * j) + threadIdx.x * (R::kD < 16 ? R::kD : 16);
+  };
+  auto request = [&](int m, int s) {
+    if (m < P.M) {
+      const size_t row = static_cast<size_t>(m) * P.K;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int c = tid + i * step;
+        if (kFull || c < chunks) {
+          copy_async<16>(smem_u32(z_at(s, i)), reinterpret_cast<const uint4*>(static_cast<const T*>(P.z) + row) + c);
+          const uint8_t* d =
+              reinterpret_cast<const uint8_t*>(static_cast<const TD*>(P.dv) + row + static_cast<size_t>(c) * N);
+          if constexpr (R::kD < 16) {
+            copy_async<8>(smem_u32(d_at(s, i, 0)), d);
+          } else {
+#pragma unroll
+            for (int j = 0; j < R::kD / 16; ++j) copy_async<16>(smem_u32(d_at(s, i, j)), d + 16 * j);
+          }
+        }
+      }
+    }
+    copy_async_commit();  // a group for every token, also past the last
+  };
+  auto z_of = [&](int s, int i, f32x2 (&z)[NP]) { to_pairs<T>(*reinterpret_cast<const uint4*>(z_at(s, i)), z); };
+  auto d_of = [&](int s, int i, f32x2 (&d)[NP]) {
+    GradChunk<TD, N> dc;
+    if constexpr (R::kD < 16) {
+      const uint2 h = *reinterpret_cast<const uint2*>(d_at(s, i, 0));
+      dc.w[0] = make_uint4(h.x, h.y, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < R::kD / 16; ++j) dc.w[j] = *reinterpret_cast<const uint4*>(d_at(s, i, j));
+    }
+    dc.get(d);
+  };
+
+  // The sums of z^2 and gd * z over this warp's part of the token in stage s.
+  auto sums_of = [&](int s) {
+    f32x2 sq2 = 0, dot2 = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
-      if (c < chunks) {
-        zc[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.z) + row) + c);
-        dc[i].load(static_cast<const TD*>(P.dv) + row + static_cast<size_t>(c) * N);
+      if (kFull || c < chunks) {
+        f32x2 z[NP], d[NP];
+        z_of(s, i, z);
+        d_of(s, i, d);
+        if constexpr (kGain) {
+#pragma unroll
+          for (int e = 0; e < NP; ++e) d[e] = mul2(d[e], gains[i][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+          sq2 = fma2(z[e], z[e], sq2);
+          dot2 = fma2(d[e], z[e], dot2);
+        }
       }
     }
+    float a0, a1, b0, b1;
+    split2(sq2, a0, a1);
+    split2(dot2, b0, b1);
+    return warp_sum2(pack2(a0 + a1, b0 + b1));
   };
-  int m = g0, parity = 0;
-  if (m < P.M) fetch(m);
-  for (; m < P.M; m += stride, parity ^= 1) {
+
+  request(g0, 0);
+  request(g0 + stride, 1);
+  copy_async_wait<1>();
+  f32x2 both = 0;
+  if (g0 < P.M) both = sums_of(0);
+  if (W > 1) {
+    if (lane == 0) red[0][group * W + wig] = both;
+    group_sync(bar, 32 * W);
+  }
+  int parity = 0, s = 0;
+  for (int m = g0; m < P.M; m += stride, parity ^= 1) {
     const size_t row = static_cast<size_t>(m) * P.K;
+    const int s1 = s == 2 ? 0 : s + 1, s2 = s1 == 2 ? 0 : s1 + 1;
     uint4 in[C];
     if (P.dz_in) {
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int c = tid + i * step;
-        if (c < chunks) in[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.dz_in) + row) + c);
+        if (kFull || c < chunks)
+          in[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.dz_in) + row) + c);
       }
     }
-    double ss = 0.0;
-    float dot = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = tid + i * step;
-      if (c < chunks) {
-        float z[N], d[N];
-        unpack16<T>(zc[i], z);
-        dc[i].get(d);
-        if constexpr (kGain) {
-          float g[N];
-          load_f32<N>(P.gain + static_cast<size_t>(c) * N, g);
-#pragma unroll
-          for (int e = 0; e < N; ++e) dot = fmaf(d[e] * g[e], z[e], dot);
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) dot = fmaf(d[e], z[e], dot);
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const double t = static_cast<double>(z[e]);
-          ss = __fma_rn(t, t, ss);
-        }
-      }
-    }
-    ss = warp_reduce(ss, [](double a, double b) { return __dadd_rn(a, b); });
-    dot = warp_reduce(dot, [](float a, float b) { return a + b; });
+    request(m + 2 * stride, s2);  // the stage of the token before: this thread has used all it read there
+    copy_async_wait<1>();
+    // The next token's sums, posted a whole token ahead of their use.
+    f32x2 next = 0;
+    if (m + stride < P.M) next = sums_of(s1);
     if (W > 1) {
-      SumPair* slot = red[parity] + group * W;
-      if (lane == 0) slot[wig] = SumPair{ss, dot};
-      group_sync(bar, 32 * W);
-      ss = slot[0].ss;
-      dot = slot[0].dot;
-      for (int i = 1; i < W; ++i) {
-        ss = __dadd_rn(ss, slot[i].ss);
-        dot += slot[i].dot;
-      }
+      if (lane == 0) red[parity ^ 1][group * W + wig] = next;
+      both = warp_sum2(lane < W ? red[parity][group * W + lane] : 0);
     }
-    const float r = rstd_of(ss, P.K, P.eps);
-    const float mean = dot * r / static_cast<float>(P.K);
-    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row);
-    uint4 zo[C];
-    GradChunk<TD, N> dn[C];
+    float ss, dot;
+    split2(both, ss, dot);
+    both = next;
+    float r = rsqrtf(fmaf(ss, P.inv_kf, P.eps));
+    if (!(ss > kSquaresLow && ss < kSquaresHigh)) {  // the same in the whole group
+      double t = 0.0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      zo[i] = zc[i];
-      dn[i] = dc[i];
+      for (int i = 0; i < C; ++i) {
+        if (kFull || tid + i * step < chunks) {
+          f32x2 z[NP];
+          z_of(s, i, z);
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            float lo, hi;
+            split2(z[e], lo, hi);
+            t = __fma_rn(static_cast<double>(lo), static_cast<double>(lo), t);
+            t = __fma_rn(static_cast<double>(hi), static_cast<double>(hi), t);
+          }
+        }
+      }
+      if (W > 1) group_sync(bar, 32 * W);  // red_d may still be read for an earlier token
+      t = group_reduce(t, [](double a, double b) { return __dadd_rn(a, b); }, red_d + group * W, W, wig, lane, bar);
+      r = rstd_of(t, P.K, P.inv_k, P.eps);
     }
-    if (m + stride < P.M) fetch(m + stride);
+    const float mean = dot * r * P.inv_kf;
+    const f32x2 r2 = pack2(r, r), mean2 = pack2(-mean, -mean);
+    uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
-      if (c < chunks) {
-        float z[N], d[N], o[N];
-        unpack16<T>(zo[i], z);
-        dn[i].get(d);
+      if (kFull || c < chunks) {
+        f32x2 n[NP], d[NP], o[NP];
+        z_of(s, i, n);
+        d_of(s, i, d);
         if (P.dz_in) {
-          unpack16<T>(in[i], o);
+          to_pairs<T>(in[i], o);
         } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) o[e] = 0.0f;
+          for (int e = 0; e < NP; ++e) o[e] = 0;
         }
-        float g[N];
-        if constexpr (kGain) load_f32<N>(P.gain + static_cast<size_t>(c) * N, g);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float n = z[e] * r;
-          if constexpr (kGain) acc[i][e] = fmaf(d[e], n, acc[i][e]);
-          const float gd = kGain ? d[e] * g[e] : d[e];
-          o[e] = fmaf(r, fmaf(-n, mean, gd), o[e]);
+        for (int e = 0; e < NP; ++e) n[e] = mul2(n[e], r2);
+        if constexpr (kGain) {
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            acc[i][e] = fma2(d[e], n[e], acc[i][e]);
+            d[e] = mul2(d[e], gains[i][e]);
+          }
         }
-        out[c] = pack16<T>(o);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) o[e] = fma2(r2, fma2(n[e], mean2, d[e]), o[e]);
+        out[c] = from_pairs<T>(o);
       }
     }
+    if (W > 1) group_sync(bar, 32 * W);
+    s = s1;
   }
   if constexpr (kGain) {
     if (P.part) {
-      float* pr = P.part + static_cast<size_t>(g0) * P.K;
+      // One row of sums per block: its groups' rows meet in the ring, in order.
+      float* out = P.part + static_cast<size_t>(blockIdx.x) * P.K;
+      float* own = groups > 1 ? reinterpret_cast<float*>(ring) + group * P.K : out;
+      if (groups > 1) {
+        copy_async_wait<0>();
+        __syncthreads();
+      }
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int c = tid + i * step;
-        if (c < chunks) {
-#pragma unroll
-          for (int e = 0; e < N / 4; ++e)
-            reinterpret_cast<float4*>(pr + static_cast<size_t>(c) * N)[e] =
-                make_float4(acc[i][4 * e], acc[i][4 * e + 1], acc[i][4 * e + 2], acc[i][4 * e + 3]);
+        if (kFull || c < chunks) store_pairs<NP>(own + static_cast<size_t>(c) * N, acc[i]);
+      }
+      if (groups > 1) {
+        __syncthreads();
+        for (int k = threadIdx.x; k < P.K; k += blockDim.x) {
+          float t = reinterpret_cast<const float*>(ring)[k];
+          for (int g = 1; g < groups; ++g) t += reinterpret_cast<const float*>(ring)[g * P.K + k];
+          out[k] = t;
         }
       }
     }
@@ -501,8 +819,8 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(const AddNorm
 // Tokens longer than the registers hold: one block per token reads it twice
 // (the second time from L2) and leaves 1 / rms in rstd for the gain's gradient.
 template <typename T, typename TD>
-__global__ void __launch_bounds__(512) add_rmsnorm_backward_long_kernel(const AddNormBackParams P) {
-  constexpr int N = kPer<T>;
+__global__ void __launch_bounds__(512, 2) add_rmsnorm_backward_long_kernel(const AddNormBackParams P) {
+  constexpr int N = kPer<T>, NP = kPairs<T>;
   __shared__ double red_d[kMaxGroupWarps];
   __shared__ float red_f[kMaxGroupWarps];
   griddep_launch_dependents();
@@ -513,49 +831,54 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_long_kernel(const Ad
   const uint4* zr = reinterpret_cast<const uint4*>(static_cast<const T*>(P.z) + row);
   const TD* dr = static_cast<const TD*>(P.dv) + row;
   double ss = 0.0;
-  float dot = 0.0f;
-  auto chunk = [&](int c, float (&z)[N], float (&d)[N], float (&gd)[N]) {
-    unpack16<T>(__ldcg(zr + c), z);
+  f32x2 dot2 = 0;
+  auto chunk = [&](int c, f32x2 (&z)[NP], f32x2 (&gd)[NP]) {
+    to_pairs<T>(__ldcg(zr + c), z);
     GradChunk<TD, N> dc;
     dc.load(dr + static_cast<size_t>(c) * N);
-    dc.get(d);
+    dc.get(gd);
     if (P.gain) {
-      float g[N];
-      load_f32<N>(P.gain + static_cast<size_t>(c) * N, g);
+      f32x2 g[NP];
+      load_pairs(P.gain + static_cast<size_t>(c) * N, g);
 #pragma unroll
-      for (int e = 0; e < N; ++e) gd[e] = d[e] * g[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) gd[e] = d[e];
+      for (int e = 0; e < NP; ++e) gd[e] = mul2(gd[e], g[e]);
     }
   };
+#pragma unroll 2
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    float z[N], d[N], gd[N];
-    chunk(c, z, d, gd);
+    f32x2 z[NP], gd[NP];
+    chunk(c, z, gd);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const double t = static_cast<double>(z[e]);
-      ss = __fma_rn(t, t, ss);
-      dot = fmaf(gd[e], z[e], dot);
+    for (int e = 0; e < NP; ++e) {
+      float lo, hi;
+      split2(z[e], lo, hi);
+      ss = __fma_rn(static_cast<double>(lo), static_cast<double>(lo), ss);
+      ss = __fma_rn(static_cast<double>(hi), static_cast<double>(hi), ss);
+      dot2 = fma2(gd[e], z[e], dot2);
     }
   }
+  float dot, dot_hi;
+  split2(dot2, dot, dot_hi);
+  dot += dot_hi;
   ss = group_reduce(ss, [](double a, double b) { return __dadd_rn(a, b); }, red_d, W, warp, lane, 1);
   dot = group_reduce(dot, [](float a, float b) { return a + b; }, red_f, W, warp, lane, 1);
-  const float r = rstd_of(ss, P.K, P.eps);
-  const float mean = dot * r / static_cast<float>(P.K);
+  const float r = rstd_of(ss, P.K, P.inv_k, P.eps);
+  const float mean = dot * r * P.inv_kf;
+  const f32x2 r2 = pack2(r, r), mean2 = pack2(-mean, -mean);
   if (P.rstd && threadIdx.x == 0) P.rstd[m] = r;
+#pragma unroll 2
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    float z[N], d[N], gd[N], o[N];
-    chunk(c, z, d, gd);
+    f32x2 z[NP], gd[NP], o[NP];
+    chunk(c, z, gd);
     if (P.dz_in) {
-      unpack16<T>(__ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.dz_in) + row) + c), o);
+      to_pairs<T>(__ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.dz_in) + row) + c), o);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = 0.0f;
+      for (int e = 0; e < NP; ++e) o[e] = 0;
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = fmaf(r, fmaf(-(z[e] * r), mean, gd[e]), o[e]);
-    reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row)[c] = pack16<T>(o);
+    for (int e = 0; e < NP; ++e) o[e] = fma2(r2, fma2(mul2(z[e], r2), mean2, gd[e]), o[e]);
+    reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row)[c] = from_pairs<T>(o);
   }
 }
 
@@ -563,49 +886,66 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_long_kernel(const Ad
 // thread per chunk of columns, block row p.
 template <typename T, typename TD>
 __global__ void __launch_bounds__(256) gain_grad_long_kernel(const AddNormBackParams P, int rows) {
-  constexpr int N = kPer<T>;
+  constexpr int N = kPer<T>, NP = kPairs<T>;
   griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= P.K / N) return;
-  float acc[N] = {};
+  f32x2 acc[NP] = {};
+#pragma unroll 4
   for (int m = blockIdx.y; m < P.M; m += rows) {
     const size_t at = static_cast<size_t>(m) * P.K + static_cast<size_t>(c) * N;
-    float z[N], d[N];
-    unpack16<T>(__ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.z) + at)), z);
+    f32x2 z[NP], d[NP];
+    to_pairs<T>(__ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.z) + at)), z);
     GradChunk<TD, N> dc;
     dc.load(static_cast<const TD*>(P.dv) + at);
     dc.get(d);
     const float r = __ldcg(P.rstd + m);
+    const f32x2 r2 = pack2(r, r);
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = fmaf(d[e], z[e] * r, acc[e]);
+    for (int e = 0; e < NP; ++e) acc[e] = fma2(d[e], mul2(z[e], r2), acc[e]);
   }
-  float* pr = P.part + static_cast<size_t>(blockIdx.y) * P.K + static_cast<size_t>(c) * N;
-#pragma unroll
-  for (int e = 0; e < N / 4; ++e)
-    reinterpret_cast<float4*>(pr)[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+  store_pairs<NP>(P.part + static_cast<size_t>(blockIdx.y) * P.K + static_cast<size_t>(c) * N, acc);
 }
 
 // dgain[k] = the sum of the partial rows in a fixed order: 32 columns per
-// block, warp w rows w, w + 32, ..., then the warps in order.
+// block, four to a thread; 128 threads share a column's rows, so that the 592
+// rows of a full grid are one batch of loads, then the warps in order.
 __global__ void __launch_bounds__(1024) gain_grad_finish_kernel(const float* __restrict__ part, int rows, int K,
                                                                 float* __restrict__ dgain) {
-  __shared__ float sums[32][33];
+  __shared__ float sums[32][32];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k = blockIdx.x * 32 + lane;  // K % 64 == 0: always inside
-  float a = 0.0f;
-#pragma unroll 4
-  for (int p = warp; p < rows; p += 32) a += __ldcg(part + static_cast<size_t>(p) * K + k);
-  sums[warp][lane] = a;
+  const int q = threadIdx.x & 7, first = threadIdx.x >> 3;
+  const float* p = part + blockIdx.x * 32 + 4 * q;  // K % 64 == 0: always inside
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 5
+  for (int i = first; i < rows; i += 128) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + static_cast<size_t>(i) * K));
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o *= 2) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+  }
+  if (lane < 8) *reinterpret_cast<float4*>(&sums[warp][4 * q]) = a;
   __syncthreads();
   if (warp == 0) {
     float t = sums[0][lane];
+#pragma unroll
     for (int i = 1; i < 32; ++i) t += sums[i][lane];
-    dgain[k] = t;
+    dgain[blockIdx.x * 32 + lane] = t;
   }
 }
+
+constexpr int kRingMax = 220 * 1024;  // of an SM's shared memory
 
 // How the backward splits its work: from the sizes and the SM count alone, so
 // the workspace figure and the launch agree.
@@ -613,41 +953,63 @@ struct BackPlan {
   int W, C, threads, grid, rows;  // C = 0: the long form; rows of the partial gain gradient
 };
 
-BackPlan plan_backward(int M, int K, int per) {
+BackPlan plan_backward(int M, int K, int per, int piece) {
   BackPlan p;
   const int chunks = K / per;
   const int sms = num_sms();
-  p.W = (chunks + 31) / 32;
-  if (p.W > kMaxGroupWarps) p.W = kMaxGroupWarps;
-  const int n = (chunks + 32 * p.W - 1) / (32 * p.W);
-  if (n > 4) {
+  // Chunks per thread: one while a warp holds the token, two while eight do, else four.
+  p.C = chunks <= 32 ? 1 : chunks <= 512 ? 2 : 4;
+  p.W = (chunks + 32 * p.C - 1) / (32 * p.C);
+  const int groups = p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
+  p.threads = 32 * p.W * groups;
+  const int ring = 3 * p.C * p.threads * piece;
+  if (p.W > kMaxGroupWarps || ring > kRingMax) {
     p.C = 0;
+    p.W = kMaxGroupWarps;
     p.threads = 32 * kMaxGroupWarps;
     p.grid = M;
     p.rows = M < 64 ? M : 64;
     return p;
   }
-  p.C = n <= 1 ? 1 : n <= 2 ? 2 : 4;
-  const int groups = p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
-  p.threads = 32 * p.W * groups;
-  const int resident = p.C > 2 ? 1 : p.threads > kNormThreads ? 2 : 4;
+  // What the registers (64, 80 or 128 a thread) and the ring (`piece` bytes a
+  // chunk, three stages) let be resident.
+  int resident = (p.C == 1 ? 1024 : p.C == 2 ? 768 : 512) / p.threads;
+  const int by_ring = kRingMax / (ring + 1024) + (ring + 1024 > kRingMax);
+  if (resident > by_ring) resident = by_ring;
   const int need = (M + groups - 1) / groups;
   p.grid = need < resident * sms ? need : resident * sms;
-  p.rows = p.grid * groups;
+  p.rows = p.grid;
   return p;
+}
+
+template <typename T, typename TD, int C, bool kGain, bool kFull>
+cudaError_t launch_back_k(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(add_rmsnorm_backward_kernel<T, TD, C, kGain, kFull>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMax);
+  });
+  if (e != cudaSuccess) return e;
+  return launch(add_rmsnorm_backward_kernel<T, TD, C, kGain, kFull>, dim3(p.grid), dim3(p.threads),
+                BackRing<T, TD>::bytes(p.threads, C), stream, true, P, p.W);
+}
+
+template <typename T, typename TD, bool kGain, bool kFull>
+cudaError_t launch_back_f(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
+  if (p.C == 1) return launch_back_k<T, TD, 1, kGain, kFull>(P, p, stream);
+  if (p.C == 2) return launch_back_k<T, TD, 2, kGain, kFull>(P, p, stream);
+  return launch_back_k<T, TD, 4, kGain, kFull>(P, p, stream);
 }
 
 template <typename T, typename TD, bool kGain>
 cudaError_t launch_back_c(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
-  const dim3 g(p.grid), b(p.threads);
-  if (p.C == 1) return launch(add_rmsnorm_backward_kernel<T, TD, 1, kGain>, g, b, 0, stream, true, P, p.W);
-  if (p.C == 2) return launch(add_rmsnorm_backward_kernel<T, TD, 2, kGain>, g, b, 0, stream, true, P, p.W);
-  return launch(add_rmsnorm_backward_kernel<T, TD, 4, kGain>, g, b, 0, stream, true, P, p.W);
+  return P.K / kPer<T> == p.C * 32 * p.W ? launch_back_f<T, TD, kGain, true>(P, p, stream)
+                                         : launch_back_f<T, TD, kGain, false>(P, p, stream);
 }
 
 template <typename T, typename TD>
 cudaError_t launch_back_t(AddNormBackParams P, float* dgain, cudaStream_t stream) {
-  const BackPlan p = plan_backward(P.M, P.K, kPer<T>);
+  const BackPlan p = plan_backward(P.M, P.K, kPer<T>, BackRing<T, TD>::kChunk);
   if (!dgain) P.part = nullptr;
   cudaError_t e;
   if (p.C == 0) {
@@ -674,26 +1036,31 @@ cudaError_t launch_add_rmsnorm_quant(const void* x, const void* residual, int x_
                                      float eps, void* z, void* x_norm, int8_t* xq, float* scale, int32_t* rowsum,
                                      cudaStream_t stream, bool pdl) {
   if (M <= 0) return cudaSuccess;
-  const AddNormParams P{x, residual, gain, eps, z, x_norm, xq, scale, rowsum, M, K};
+  const AddNormParams P{x, residual, gain, eps, z, x_norm, xq, scale, rowsum, M, K, 1.0 / K};
   return x_bf16 ? launch_add_rmsnorm_quant_t<__nv_bfloat16>(P, stream, pdl)
                 : launch_add_rmsnorm_quant_t<float>(P, stream, pdl);
 }
 
-size_t add_rmsnorm_backward_scratch_bytes(int M, int K, int x_bf16) {
+// Partial rows, then 1 / rms of the long form; for dv of either type.
+static size_t part_bytes(int M, int K, int z_bf16) {
+  const int per = z_bf16 ? 8 : 4;
+  const BackPlan a = plan_backward(M, K, per, 16 + 2 * per), b = plan_backward(M, K, per, 16 + 4 * per);
+  return r256(static_cast<size_t>(a.rows > b.rows ? a.rows : b.rows) * K * 4);
+}
+
+size_t add_rmsnorm_backward_scratch_bytes(int M, int K, int z_bf16) {
   if (M <= 0 || K <= 0) return 0;
-  const BackPlan p = plan_backward(M, K, x_bf16 ? 8 : 4);
-  return r256(static_cast<size_t>(p.rows) * K * 4) + r256(static_cast<size_t>(M) * 4);
+  return part_bytes(M, K, z_bf16) + r256(static_cast<size_t>(M) * 4);
 }
 
 cudaError_t launch_add_rmsnorm_backward(const void* z, int z_bf16, const void* dnorm, int dnorm_bf16, int M, int K,
                                         const float* gain, float eps, const void* dz_in, void* dz, float* dgain,
                                         uint8_t* scratch, cudaStream_t stream) {
   if (M <= 0) return cudaSuccess;
-  AddNormBackParams P{z, dnorm, gain, dz_in, eps, dz, nullptr, nullptr, M, K};
+  AddNormBackParams P{z, dnorm, gain, dz_in, eps, dz, nullptr, nullptr, M, K, 1.0 / K, static_cast<float>(1.0 / K)};
   if (scratch) {
-    const BackPlan p = plan_backward(M, K, z_bf16 ? 8 : 4);
     P.part = reinterpret_cast<float*>(scratch);
-    P.rstd = reinterpret_cast<float*>(scratch + r256(static_cast<size_t>(p.rows) * K * 4));
+    P.rstd = reinterpret_cast<float*>(scratch + part_bytes(M, K, z_bf16));
   }
   if (z_bf16)
     return dnorm_bf16 ? launch_back_t<__nv_bfloat16, __nv_bfloat16>(P, dgain, stream)

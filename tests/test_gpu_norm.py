@@ -7,18 +7,22 @@ against ``rmsnorm_quant`` on z.
 Backward, against the formula in 64 bits.  The bar counts the kernel's fp32
 roundings, u = 2^-24 each, on the absolute terms of the formula.  With
 n = z r and D = (r / K) sum |gd z|:
-  * gd (1 rounding), r (its one rounding from 64 bits, squared into n and the
-    outer factor), n, the two fused steps and the sum: at most 8 u of
+  * r: a square passes the thread's chain (its product fused, at most 16 terms
+    a half), the join of two halves and two trees of 5 steps, so the sum is off
+    by 27 u, the mean with eps by 29 u, and r by half of that and 2 units in
+    the last place (4 u) of rsqrtf: R = 18.5 u;
+  * r gd: R, gd, the two fused steps, 21.5 u; r n mean: R twice, n, the two
+    fused steps, 40 u; dz_in: 1 u.  So at most 40 u of
     |r gd| + |r n mean| + |dz_in|;
-  * the dot product sum gd z: a term passes its own rounding, the thread's
-    chain (at most 32 terms when held in registers, K / 512 otherwise), 5
-    shuffles, 16 warps, then the products with r and 1 / K: DEPTH u of D,
-    times |r n|;
+  * mean: a term of the dot product passes its own rounding, the thread's
+    chain (at most 32 terms when held in registers, K / 512 otherwise), the
+    join of two halves, 5 shuffles, 5 more or 16 warps, then R and the roundings of the
+    products with r and 1 / K and of 1 / K: DEPTH u of D, times |r n|;
   * the last rounding to the output type: eps / 2 of |dz|.
-dgain: a term dnorm n has 3 roundings, then the chain over a group's tokens
-(at most ceil(M / 64): there are at least 64 groups, or one token each), the
-148 partial rows that a warp of the closing kernel takes at most and its 32
-warps.
+dgain: a term dnorm n has R, n and the fused step, at most 21 u, then the
+chain over a group's tokens (at most ceil(M / 64): there are at least 64
+groups, or one token each), the 148 partial rows that a warp of the closing
+kernel takes at most and its 32 warps.
 """
 import threading
 
@@ -55,8 +59,10 @@ FORWARD = [
     (1, 64, "bf16", True, 1e-6), (1, 2560, "bf16", True, 1e-6), (3, 64, "f32", False, 1e-5), (16, 8192, "bf16", True, 1e-6),
     (7, 3200, "f32", True, 1e-6), (33, 8640, "f32", False, 1e-6), (5, 192, "bf16", True, 0.0), (2048, 2560, "bf16", True, 1e-5),
     (3000, 64, "bf16", True, 1e-6), (2500, 320, "f32", True, 1e-6), (2, 32768, "bf16", True, 1e-6),
-    (2, 16384, "f32", True, 1e-6),          # the longest tokens held in registers
-    (3, 32768 + 64, "bf16", True, 1e-6), (2, 16384 + 64, "f32", False, 1e-6),  # z is read back
+    (2, 16384, "bf16", True, 1e-6), (2, 8192, "f32", True, 1e-6),              # the longest held in registers
+    (3, 16384 + 64, "bf16", True, 1e-6), (2, 8192 + 64, "f32", False, 1e-6),   # held in shared memory
+    (2, 114688, "bf16", True, 1e-6), (2, 57344, "f32", True, 1e-6),            # the longest held there
+    (3, 114688 + 64, "bf16", True, 1e-6), (2, 57344 + 64, "f32", False, 1e-6),  # z is read back
     (1100, 8192, "bf16", False, 1e-6),
 ]
 
@@ -89,7 +95,7 @@ def test_forward_parity(M, K, dtype, with_gain, eps):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("K", [256, 40960])
+@pytest.mark.parametrize("K", [256, 40960, 131072])
 def test_forward_degenerate_tokens(dtype, K):
     """Zero, one-hot, cancelling, huge and tiny tokens, and tokens with infinities and NaN: whatever rmsnorm_quant
     makes of z, and the other tokens untouched by them."""
@@ -153,14 +159,14 @@ def test_backward_parity(M, K, dtype, grad, with_gain, past):
     gdev = None if g is None else dev(g)
     dz, dgain = tb.add_rmsnorm_backward(z, d, gdev, eps=eps, dz_in=i)
     want, wg, terms, dots, tg = _back_ref(zf, df, g, eps, inf)
-    depth = 1 + max(32, -(-K // 512)) + 5 + 16 + 3
-    bar = U * (8 * terms + depth * dots) + torch.finfo(dt).eps / 2 * np.abs(want) * (1 + 2.0 ** -8)
+    depth = 1 + max(32, -(-K // 512)) + 1 + 5 + 16 + 19 + 3
+    bar = U * (40 * terms + depth * dots) + torch.finfo(dt).eps / 2 * np.abs(want) * (1 + 2.0 ** -8)
     err = np.abs(dz.float().cpu().numpy().astype(np.float64) - want)
     assert (err <= bar).all(), (err / bar).max()
     if g is None:
         assert dgain is None
     else:
-        bar = U * (3 + -(-M // 64) + 148 + 32) * tg
+        bar = U * (21 + -(-M // 64) + 148 + 32) * tg
         err = np.abs(dgain.cpu().numpy().astype(np.float64) - wg)
         assert (err <= bar).all(), (err / bar).max()
     # again, in place of dz_in, and without the gain's gradient: the same
@@ -202,8 +208,8 @@ def test_backward_of_large_and_zero_rows():
     """Rows far out of range for r^3 in fp32, and zero rows (r = 1 / sqrt(eps))."""
     M, K = 4, 256
     z, _ = _act(M, K, 7, torch.float32)
-    z[0] *= 1e15
-    z[1] *= 1e-12
+    z[0] *= 1e25  # squares beyond fp32
+    z[1] *= 1e-22
     z[2] = 0
     d, df = _act(M, K, 8, torch.float32)
     want, *_ = _back_ref(z.cpu().numpy(), df, None, 1e-6, None)
@@ -226,7 +232,7 @@ def test_empty_batch():
 @pytest.mark.gpu
 def test_no_writes_outside_outputs():
     pad, canary = 4096, 0x5A
-    for M, K, dt in ((3, 192, torch.bfloat16), (5, 40960, torch.bfloat16), (1, 64, torch.float32)):
+    for M, K, dt in ((3, 192, torch.bfloat16), (5, 40960, torch.bfloat16), (1, 64, torch.float32), (2, 65536, torch.float32)):
         x, _ = _act(M, K, 1, dt)
         d, _ = _act(M, K, 2, dt)
         g = torch.ones(K, device="cuda")
