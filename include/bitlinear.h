@@ -352,9 +352,10 @@ size_t bitlinear_i8_workspace_bytes(int M, int N, int K);
  *   acc_out device int32 [M][N] out, or NULL: the exact accumulators.
  *   workspace / workspace_bytes: >= bitlinear_i8_workspace_bytes(M, N, K),
  *           its first 256 bytes zero.
- * K <= 131008 (the int32 sums).  M <= 32 streams the weights through a decode
- * kernel; larger M runs on the tensor cores (tcgen05); bitlinear_set_path
- * forces either (its GEMV takes M <= 32 here).  Both give the same
+ * K <= 131008 (the int32 sums).  Few tokens (M <= 8; up to 16 or 32 on small
+ * matrices) stream the weights through a decode kernel; the rest runs on the
+ * tensor cores (tcgen05); bitlinear_set_path forces either (its GEMV takes
+ * M <= 32 here).  Both give the same
  * accumulators and outputs, bit for bit.  Unlike the packed weights of the
  * other products, wq may be written by the kernel just before the call.
  * y, acc_out and the workspace overlap no other argument.  Every pointer

@@ -472,7 +472,7 @@ static int check_i8(int N, int K, int M, int y_dtype) {
 }
 
 static int launch_i8(const bl::I8Args& a, cudaStream_t s) {
-  const bool gemv = g_path == 1 || (g_path == 0 && a.M <= bl::kI8GemvMaxTokens);
+  const bool gemv = g_path == 1 || (g_path == 0 && bl::i8_takes_gemv(a.M, a.N, a.K));
   cudaError_t e = gemv ? bl::launch_i8_gemv(a, s, true) : bl::launch_i8_gemm(a, s, true);
   return e == cudaSuccess ? BL_OK : cuda_fail(e, "8-bit product launch");
 }

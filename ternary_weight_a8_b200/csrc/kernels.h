@@ -207,6 +207,7 @@ struct I8Args {
 };
 constexpr int kI8MaxK = 131008;       // 128 * 128 * K < 2^31
 constexpr int kI8GemvMaxTokens = 32;
+bool i8_takes_gemv(int M, int N, int K);  // the decode kernel's sizes
 cudaError_t launch_i8_gemv(const I8Args& a, cudaStream_t stream, bool pdl);  // M <= kI8GemvMaxTokens
 cudaError_t launch_i8_gemm(const I8Args& a, cudaStream_t stream, bool pdl);
 
