@@ -295,11 +295,14 @@ class _Call:
 
     def new(self, shape, dtype, zero: bool = False) -> torch.Tensor:
         """An output of the call, from its stream's memory."""
-        make = self.like.new_zeros if zero else self.like.new_empty
         if self.stream is None:
-            return make(shape, dtype=dtype)
+            if zero:
+                return self.like.new_zeros(shape, dtype=dtype)
+            if shape == self.like.shape:
+                return torch.empty_like(self.like, dtype=dtype)  # the cheapest of torch's ways
+            return self.like.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            t = make(shape, dtype=dtype)
+            t = self.like.new_zeros(shape, dtype=dtype) if zero else self.like.new_empty(shape, dtype=dtype)
         t.record_stream(torch.cuda.current_stream(self.index))  # the caller may use it there
         return t
 

@@ -527,8 +527,8 @@ int bitlinear_forward_i8(const int8_t* wq, const float* wscale, int N, int K, co
   int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   const int ldq = code_pitch(K);
-  cudaError_t e = bl::launch_act_quant(x, x_dtype == BL_BF16, M, K, ldq, xq, scale, nullptr, s, true);
-  if (e != cudaSuccess) return cuda_fail(e, "act_quant launch");
+  cudaError_t e = bl::launch_row_codes(x, x_dtype == BL_BF16, M, K, ldq, xq, scale, s, true);
+  if (e != cudaSuccess) return cuda_fail(e, "activation codes launch");
   return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, ldq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
                               acc_out, static_cast<uint32_t*>(workspace)},
                    s);

@@ -192,6 +192,11 @@ cudaError_t launch_ste_backward(const uint8_t* packed, const float* gamma, int N
                                 const float* scale, int M, void* dx, bool dx_bf16, float* dw, uint8_t* scratch,
                                 uint32_t* status, cudaStream_t stream);
 
+// The codes of rows of activations, as launch_act_quant makes them (no code
+// sums); rows of ldq bytes, zero past K.
+cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int ldq, int8_t* xq, float* scale,
+                             cudaStream_t stream, bool pdl);
+
 // The 8-bit product: y = acc / (s[m] * ws[n]) with acc = sum_k xq[m][k] * wq[n][k] in int32.
 struct I8Args {
   const int8_t* wq;      // [N][K]

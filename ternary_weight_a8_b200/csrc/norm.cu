@@ -182,7 +182,22 @@ __device__ __forceinline__ int store_codes(const uint4& v, f32x2 s2, int8_t* dst
   return sum;
 }
 
-// The same for a token with infinities or NaN: NaN products (NaN * s, and
+// The largest |value| of a chunk that is no NaN.
+template <typename T>
+__device__ __forceinline__ float absmax_any(const uint4& v) {
+  f32x2 p[kPairs<T>];
+  to_pairs<T>(v, p);
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < kPairs<T>; ++e) {
+    float lo, hi;
+    split2(p[e], lo, hi);
+    m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
+  }
+  return m;
+}
+
+// Codes for a token with infinities or NaN: NaN products (NaN * s, and
 // infinity * 0, since an infinity makes s zero) give code 0.
 template <typename T>
 __device__ __forceinline__ int store_codes_any(const uint4& v, float s, int8_t* dst) {
@@ -425,16 +440,7 @@ __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_qua
   } else {
     // Infinities or NaN: the largest |value| that is a number or an infinity.
     amax = 0.0f;
-    for_each([&](const uint4& v, int) {
-      f32x2 p[kPairs<T>];
-      to_pairs<T>(v, p);
-#pragma unroll
-      for (int e = 0; e < kPairs<T>; ++e) {
-        float lo, hi;
-        split2(p[e], lo, hi);
-        amax = fmaxf(amax, fmaxf(fabsf(lo), fabsf(hi)));
-      }
-    });
+    for_each([&](const uint4& v, int) { amax = fmaxf(amax, absmax_any<T>(v)); });
     amax = group_reduce(amax, [](float a, float b) { return fmaxf(a, b); }, red_f + group * W, W, wig, lane, bar);
     s = __fdiv_rn(127.0f, fmaxf(amax, 1e-5f));
     for_each([&](const uint4& v, int c) {
@@ -455,31 +461,40 @@ __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_qua
   if (tid == 0) P.scale[m] = s;
 }
 
-template <typename T>
-cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stream, bool pdl) {
-  const int chunks = P.K / kPer<T>;
-  // Chunks per thread n and warps per token W: four chunks per thread (the
-  // most that leave 32 warps to an SM) while the tokens give every SM 16
-  // warps, else fewer chunks and more warps, as far as a block goes.
-  int W = 0, n = 0;
+// How tokens are spread: n chunks per thread (over four: more than registers
+// hold), W warps per token, `groups` tokens per block.
+struct Groups {
+  int n, W, groups;
+};
+
+Groups plan_groups(int M, int chunks) {
+  // Four chunks per thread (the most that leave 32 warps to an SM) while the
+  // tokens give every SM 16 warps, else fewer chunks and more warps, as far
+  // as a block goes.
+  Groups g{5, 0, 1};
   for (int c = 4; c >= 1; c /= 2) {
     int w = (chunks + 32 * c - 1) / (32 * c);
     if (w > 8) w = (w + 3) / 4 * 4;  // an even share of an SM's four schedulers and their registers
     if (w > kMaxGroupWarps) break;
-    W = w;
-    n = (chunks + 32 * w - 1) / (32 * w);
-    if (static_cast<long long>(P.M) * w >= 16LL * num_sms()) break;
+    g.W = w;
+    g.n = (chunks + 32 * w - 1) / (32 * w);
+    if (static_cast<long long>(M) * w >= 16LL * num_sms()) break;
   }
-  if (W == 0) {
-    // Longer than 16 warps hold.  Up to nine chunks a thread, eight warps leave
-    // room for more tokens on an SM (1021 fp32 tokens of 8640: 26.8 us, 33.0
-    // with 16 warps); longer tokens want all 16 (512 bf16 tokens of 28672:
-    // 28.2 us, 36.0 with 8).
-    W = chunks <= 9 * 32 * 8 ? 8 : kMaxGroupWarps;
-    n = 5;
-  }
-  const int groups = W > kNormThreads / 32 ? 1 : kNormThreads / 32 / W;
-  const int threads = 32 * W * groups;
+  // Longer than 16 warps hold.  Up to nine chunks a thread, eight warps leave
+  // room for more tokens on an SM (1021 fp32 tokens of 8640: 26.8 us, 33.0
+  // with 16 warps); longer tokens want all 16 (512 bf16 tokens of 28672:
+  // 28.2 us, 36.0 with 8).
+  if (g.W == 0) g.W = chunks <= 9 * 32 * 8 ? 8 : kMaxGroupWarps;
+  g.groups = g.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / g.W;
+  if (g.n > 4) g.groups = 1;
+  return g;
+}
+
+template <typename T>
+cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stream, bool pdl) {
+  const int chunks = P.K / kPer<T>;
+  const Groups g = plan_groups(P.M, chunks);
+  const int W = g.W, n = g.n, groups = g.groups, threads = 32 * W * groups;
   const dim3 grid((P.M + groups - 1) / groups);
   const int held = n <= 2 ? n : 4;
   const bool full = chunks == held * 32 * W;  // every thread holds as many chunks as it has room for
@@ -499,6 +514,90 @@ cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stre
   if (e != cudaSuccess) return e;
   return launch(add_rmsnorm_quant_kernel<T, 0, false>, grid, dim3(threads), staged ? row : 0, stream, pdl, P, W,
                 staged ? 1 : 0);
+}
+
+// ---------------------------------------------------------------------------
+// The activation codes alone, for the 8-bit product: exactly quant_act's, on
+// the norm's arithmetic (packed products, integer maxima, groups of warps per
+// token).  Bound by memory: 3 bytes per bf16 input.
+// ---------------------------------------------------------------------------
+struct CodesParams {
+  const void* x;
+  int8_t* xq;  // rows of ldq bytes, zero past K
+  float* scale;
+  int M, K, ldq;
+};
+
+template <typename T, int C>
+__global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) row_codes_kernel(const CodesParams P, int W) {
+  constexpr int N = kPer<T>;
+  __shared__ uint32_t red_u[kMaxGroupWarps];
+  __shared__ float red_f[kMaxGroupWarps];
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, wig = warp % W, groups = (blockDim.x >> 5) / W;
+  const int m = blockIdx.x * groups + group;
+  const int tid = wig * 32 + lane, step = 32 * W, chunks = P.K / N, bar = 1 + group;
+  griddep_wait();
+  if (m >= P.M) return;  // the whole group: its named barrier is its own
+  const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(P.x) + static_cast<size_t>(m) * P.K);
+  int8_t* qr = P.xq + static_cast<size_t>(m) * P.ldq;
+  for (int c = P.K + 16 * tid; c < P.ldq; c += 16 * step) *reinterpret_cast<uint4*>(qr + c) = make_uint4(0, 0, 0, 0);
+
+  constexpr int CR = C > 0 ? C : 1;
+  uint4 keep[CR];
+  uint32_t top = 0;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (tid + i * step < chunks) keep[i] = __ldcg(xr + tid + i * step);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (tid + i * step < chunks) top = absmax16<T>(top, keep[i]);
+  } else {
+#pragma unroll 4
+    for (int c = tid; c < chunks; c += step) top = absmax16<T>(top, __ldcg(xr + c));
+  }
+  auto for_each = [&](auto&& fn) {
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (tid + i * step < chunks) fn(keep[i], tid + i * step);
+    } else {
+#pragma unroll 4
+      for (int c = tid; c < chunks; c += step) fn(__ldcg(xr + c), c);
+    }
+  };
+  top = __reduce_max_sync(0xffffffffu, absmax_bits<T>(top));
+  if (W > 1) {
+    if (lane == 0) red_u[group * W + wig] = top;
+    group_sync(bar, 32 * W);
+    for (int i = 0; i < W; ++i) top = max(top, red_u[group * W + i]);
+  }
+  float s;
+  if (top < 0x7f800000u) {
+    s = __fdiv_rn(127.0f, fmaxf(__uint_as_float(top), 1e-5f));
+    const f32x2 s2 = pack2(s, s);
+    for_each([&](const uint4& v, int c) { store_codes<T>(v, s2, qr + static_cast<size_t>(c) * N); });
+  } else {
+    // Infinities or NaN, as in the norm.
+    float amax = 0.0f;
+    for_each([&](const uint4& v, int) { amax = fmaxf(amax, absmax_any<T>(v)); });
+    amax = group_reduce(amax, [](float a, float b) { return fmaxf(a, b); }, red_f + group * W, W, wig, lane, bar);
+    s = __fdiv_rn(127.0f, fmaxf(amax, 1e-5f));
+    for_each([&](const uint4& v, int c) { store_codes_any<T>(v, s, qr + static_cast<size_t>(c) * N); });
+  }
+  if (tid == 0) P.scale[m] = s;
+}
+
+template <typename T>
+cudaError_t launch_row_codes_t(const CodesParams& P, cudaStream_t stream, bool pdl) {
+  const Groups g = plan_groups(P.M, P.K / kPer<T>);
+  const dim3 grid((P.M + g.groups - 1) / g.groups), block(32 * g.W * g.groups);
+  if (g.n <= 1) return launch(row_codes_kernel<T, 1>, grid, block, 0, stream, pdl, P, g.W);
+  if (g.n <= 2) return launch(row_codes_kernel<T, 2>, grid, block, 0, stream, pdl, P, g.W);
+  if (g.n <= 4) return launch(row_codes_kernel<T, 4>, grid, block, 0, stream, pdl, P, g.W);
+  return launch(row_codes_kernel<T, 0>, grid, block, 0, stream, pdl, P, g.W);
 }
 
 // ---------------------------------------------------------------------------
@@ -1039,6 +1138,13 @@ cudaError_t launch_add_rmsnorm_quant(const void* x, const void* residual, int x_
   const AddNormParams P{x, residual, gain, eps, z, x_norm, xq, scale, rowsum, M, K, 1.0 / K};
   return x_bf16 ? launch_add_rmsnorm_quant_t<__nv_bfloat16>(P, stream, pdl)
                 : launch_add_rmsnorm_quant_t<float>(P, stream, pdl);
+}
+
+cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int ldq, int8_t* xq, float* scale,
+                             cudaStream_t stream, bool pdl) {
+  if (M <= 0) return cudaSuccess;
+  const CodesParams P{x, xq, scale, M, K, ldq};
+  return x_bf16 ? launch_row_codes_t<__nv_bfloat16>(P, stream, pdl) : launch_row_codes_t<float>(P, stream, pdl);
 }
 
 // Partial rows, then 1 / rms of the long form; for dv of either type.

@@ -93,6 +93,31 @@ def test_quantises_activations(M, K, dtype):
     _check(y, acc, q_ref, s_ref, wq_ref, ws_ref)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(9, 192), (9, 8640), (700, 320), (2500, 64), (3, 16448), (3, 40960)])
+def test_codes_of_any_activations(M, K, dtype):
+    """The call's own codes are quant_act's: zero, tiny and huge tokens, tokens with infinities and NaN, lengths of every
+    form of the kernel; seen through the identity's rows as weights."""
+    x = torch.randn((M, K), generator=torch.Generator().manual_seed(K)).to(dtype)
+    x[0] = 0
+    x[1] *= 1e20
+    x[2, 3] = float("inf")
+    if M > 8:
+        x[3] *= 1e-30
+        x[4, 5] = float("nan")
+        x[5, 6], x[5, 7] = float("-inf"), float("nan")
+    x = x.cuda()
+    q, s, _ = tb.quant_act(x)
+    rows = torch.arange(0, K, max(1, K // 500), device="cuda")
+    eye = torch.zeros((rows.numel(), K), dtype=torch.int8, device="cuda")
+    eye[torch.arange(rows.numel(), device="cuda"), rows] = 1
+    ones = torch.ones(rows.numel(), device="cuda")
+    y, acc = tb.forward_i8(eye, ones, x, out_dtype=torch.float32, acc_out=True)
+    y2, acc2 = tb.forward_i8_quantized(eye, ones, q, s, out_dtype=torch.float32, acc_out=True)
+    assert torch.equal(acc, q[:, rows].int()) and torch.equal(acc2, acc)
+    assert torch.equal(torch.nan_to_num(y, nan=7.0), torch.nan_to_num(y2, nan=7.0))
+
+
 @pytest.mark.parametrize("M", [1, 40])
 def test_extreme_sums(M):
     """The longest sums of the largest codes: -128 * -128 * K stays inside int32."""
