@@ -1054,7 +1054,7 @@ struct BackPlan {
 
 BackPlan plan_backward(int M, int K, int per, int piece) {
   BackPlan p;
-  const int chunks = K / per;
+  const int chunks = K > per ? K / per : 1;  // (any K may be asked about)
   const int sms = num_sms();
   // Chunks per thread: one while a warp holds the token, two while eight do, else four.
   p.C = chunks <= 32 ? 1 : chunks <= 512 ? 2 : 4;

@@ -95,13 +95,13 @@ def test_forward_parity(M, K, dtype, with_gain, eps):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("K", [256, 40960, 131072])
-def test_forward_degenerate_tokens(dtype, K):
+@pytest.mark.parametrize("K,eps", [(256, 1e-6), (256, 0.0), (40960, 1e-6), (131072, 1e-6)])
+def test_forward_degenerate_tokens(dtype, K, eps):
     """Zero, one-hot, cancelling, huge and tiny tokens, and tokens with infinities and NaN: whatever rmsnorm_quant
     makes of z, and the other tokens untouched by them."""
     dt = DT[dtype]
-    x = torch.randn((9, K), generator=torch.Generator().manual_seed(K)).to(dt)
-    res = torch.randn((9, K), generator=torch.Generator().manual_seed(K + 1)).to(dt)
+    x = torch.randn((10, K), generator=torch.Generator().manual_seed(K)).to(dt)
+    res = torch.randn((10, K), generator=torch.Generator().manual_seed(K + 1)).to(dt)
     x[0], res[0] = 0, 0
     x[1], res[1] = 0, 0
     x[1, 17] = -3.0
@@ -111,16 +111,17 @@ def test_forward_degenerate_tokens(dtype, K):
     x[5, 3] = float("inf")
     x[6, 5] = float("nan")
     x[7, 5], res[7, 5] = float("inf"), float("-inf")
+    x[9], res[9] = x[9] * 1e-39, res[9] * 1e-39  # subnormal
     x, res = x.cuda(), res.cuda()
     g = dev(_gain(K, 3))
-    z, v, q, s, r = tb.add_rmsnorm_quant(x, res, g, x_norm=True)
+    z, v, q, s, r = tb.add_rmsnorm_quant(x, res, g, eps=eps, x_norm=True)
     zr = (x.float() + res.float()).to(dt)
     assert torch.equal(torch.nan_to_num(z.float(), nan=7.0), torch.nan_to_num(zr.float(), nan=7.0))
-    v2, q2, s2, r2 = tb.rmsnorm_quant(z, g, x_norm=True)
+    v2, q2, s2, r2 = tb.rmsnorm_quant(z, g, eps=eps, x_norm=True)
     assert torch.equal(q, q2) and torch.equal(r, r2)
     assert torch.equal(torch.nan_to_num(s, nan=-1.0), torch.nan_to_num(s2, nan=-1.0))
     assert torch.equal(torch.nan_to_num(v.float(), nan=7.0), torch.nan_to_num(v2.float(), nan=7.0))
-    assert not q[0].any() and not q[2].any()
+    assert not q[0].any() and not q[2].any()  # zero, or NaN (0 / 0 without an eps), is code 0
 
 
 def _back_ref(z, d, g, eps, dz_in):
@@ -144,7 +145,7 @@ BACKWARD = [
     (1500, 2560, "bf16", "f32", True, True), (700, 8192, "bf16", "bf16", True, True), (300, 8192, "f32", "f32", True, True),
     (64, 16384, "bf16", "bf16", True, True), (9, 8640, "bf16", "bf16", False, False),
     (70, 16384 + 64, "bf16", "f32", True, True), (33, 8192 + 64, "f32", "bf16", True, False),  # read twice
-    (2, 28672, "bf16", "bf16", False, True),
+    (2, 28672, "bf16", "bf16", False, True), (20, 12288, "bf16", "f32", True, True),
 ]
 
 
@@ -217,6 +218,18 @@ def test_backward_of_large_and_zero_rows():
     got = dz.cpu().numpy().astype(np.float64)
     scale = np.abs(want).max(1, keepdims=True)
     assert np.isfinite(got).all() and (np.abs(got - want) <= 1e-5 * scale).all()
+
+
+@pytest.mark.gpu
+def test_c_call_without_sums_gain_or_normalised_output():
+    M, K = 5, 320
+    x, _ = _act(M, K, 1, torch.float32)
+    want = tb.add_rmsnorm_quant(x, x)
+    z, q, s = torch.empty_like(x), torch.empty((M, K), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    rc = tb.lib().bitlinear_add_rmsnorm_quant(x.data_ptr(), x.data_ptr(), tb.BL_F32, M, K, None, 1e-6, z.data_ptr(), None,
+                                              q.data_ptr(), s.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
+    assert rc == tb.BL_OK
+    assert torch.equal(z, want[0]) and torch.equal(q, want[1]) and torch.equal(s, want[2])
 
 
 @pytest.mark.gpu

@@ -35,6 +35,8 @@ def test_workspace_grows_with_the_tokens_up_to_the_grid():
     small = tb.add_rmsnorm_backward_workspace_bytes(1, 2560, tb.torch.bfloat16)
     assert small == 256 + 2560 * 4 + 256
     assert tb.add_rmsnorm_backward_workspace_bytes(0, 2560, tb.torch.bfloat16) == 256
+    for K in (0, 1, 7, 63, 100):  # no such norm, but a size all the same
+        assert tb.add_rmsnorm_backward_workspace_bytes(3, K, tb.torch.float32) >= 256
     sizes = [tb.add_rmsnorm_backward_workspace_bytes(M, 8192, tb.torch.bfloat16) for M in (1, 64, 1 << 20)]
     assert sizes[0] < sizes[1] < sizes[2] < 256 + 4 * 148 * 8192 * 4 + (4 << 20) + 256
 
