@@ -13,6 +13,7 @@ Calls (same names as the C ABI, without the ``bitlinear_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -281,6 +282,9 @@ class _Call:
         """The address of a caller's tensor, its place, layout, shape and type checked (None for an absent one)."""
         if t is None:
             return None
+        if (t.get_device() == self.index and t.is_contiguous() and (shape is None or t.shape == shape)
+                and (dtype is None or t.dtype is dtype) and self.stream is None):
+            return t.data_ptr()
         if t.get_device() != self.index:
             raise ValueError("%s is on %s, not on %s" % (name, t.device, self.like.device))
         if not t.is_contiguous():
@@ -527,6 +531,7 @@ def quant_weights_i8(W: torch.Tensor, wq: torch.Tensor | None = None, wscale: to
     return wq, wscale
 
 
+@functools.lru_cache(maxsize=4096)
 def i8_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib().bitlinear_i8_workspace_bytes(M, N, K))
 
@@ -554,7 +559,7 @@ def forward_i8(wq: torch.Tensor, wscale: torch.Tensor, x: torch.Tensor, out_dtyp
     M = x.shape[0]
     c = _Call(x, stream)
     y, yp, ycode, acc, ap = _i8_outputs(c, M, N, out_dtype, y, acc_out)
-    wp, nbytes = c.workspace(workspace, lib().bitlinear_i8_workspace_bytes(M, N, K))
+    wp, nbytes = c.workspace(workspace, i8_workspace_bytes(M, N, K))
     c.run(lib().bitlinear_forward_i8, c.ptr(wq, "wq", None, torch.int8), c.ptr(wscale, "wscale", (N,), torch.float32), N, K,
           c.ptr(x, "x", (M, K)), _dtype_code(x.dtype), M, yp, ycode, ap, wp, nbytes)
     return y if acc is None else (y, acc)

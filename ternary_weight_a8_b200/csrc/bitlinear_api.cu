@@ -471,8 +471,10 @@ static int check_i8(int N, int K, int M, int y_dtype) {
   return BL_OK;
 }
 
+static bool i8_gemv(int M, int N, int K) { return g_path == 1 || (g_path == 0 && bl::i8_takes_gemv(M, N, K)); }
+
 static int launch_i8(const bl::I8Args& a, cudaStream_t s) {
-  const bool gemv = g_path == 1 || (g_path == 0 && bl::i8_takes_gemv(a.M, a.N, a.K));
+  const bool gemv = i8_gemv(a.M, a.N, a.K);
   cudaError_t e = gemv ? bl::launch_i8_gemv(a, s, true) : bl::launch_i8_gemm(a, s, true);
   return e == cudaSuccess ? BL_OK : cuda_fail(e, "8-bit product launch");
 }
@@ -527,6 +529,10 @@ int bitlinear_forward_i8(const int8_t* wq, const float* wscale, int N, int K, co
   int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
   const int ldq = code_pitch(K);
+  if (i8_gemv(M, N, K) && bl::i8_gemv_quantises(M, N, K, x_dtype == BL_BF16))
+    return launch_i8(bl::I8Args{wq, wscale, N, K, M, nullptr, 0, nullptr, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+                                acc_out, static_cast<uint32_t*>(workspace), x, x_dtype == BL_BF16},
+                     s);
   cudaError_t e = bl::launch_row_codes(x, x_dtype == BL_BF16, M, K, ldq, xq, scale, s, true);
   if (e != cudaSuccess) return cuda_fail(e, "activation codes launch");
   return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, ldq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,

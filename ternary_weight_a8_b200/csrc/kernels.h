@@ -209,10 +209,16 @@ struct I8Args {
   int y_type;            // OutType
   int32_t* acc_out;      // [M][N] or null
   uint32_t* status;
+  // Raw tokens [M][K], or null: the decode kernel then quantises them itself
+  // (i8_gemv_quantises) and xq, ldx and scale are not used.
+  const void* x = nullptr;
+  int x_bf16 = 0;
 };
+constexpr int kI8RawMax = 16384;      // values of raw tokens
 constexpr int kI8MaxK = 131008;       // 128 * 128 * K < 2^31
 constexpr int kI8GemvMaxTokens = 32;
-bool i8_takes_gemv(int M, int N, int K);  // the decode kernel's sizes
+bool i8_takes_gemv(int M, int N, int K);                  // the decode kernel's sizes
+bool i8_gemv_quantises(int M, int N, int K, int x_bf16);  // and those at which it takes raw tokens
 cudaError_t launch_i8_gemv(const I8Args& a, cudaStream_t stream, bool pdl);  // M <= kI8GemvMaxTokens
 cudaError_t launch_i8_gemm(const I8Args& a, cudaStream_t stream, bool pdl);
 
