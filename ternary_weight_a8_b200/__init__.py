@@ -8,7 +8,11 @@ library is missing or no GPU is present, the calls raise.
 
 Calls (same names as the C ABI, without the ``bitlinear_`` prefix):
 ``pack_weights``, ``quant_act``, ``forward``, ``forward_quantized``,
-``layer_chain``, ``device_status``, plus workspace helpers.
+``layer_chain``, ``device_status``, plus workspace helpers; around the
+ternary layers ``rmsnorm_quant``, ``add_rmsnorm_quant`` and its gradient
+``add_rmsnorm_backward``, ``glu_quant``, ``gate_up_glu``, ``ste_backward``, and
+the 8-bit product ``forward_i8`` / ``forward_i8_quantized`` with
+``quant_weights_i8``.
 """
 from __future__ import annotations
 

@@ -9,7 +9,7 @@
 // One kernel in three shapes:
 //   pair   a cluster of two CTAs shares 256 tokens x 256 channels through
 //          cta_group::2: each loads its 128 tokens and 128 of the channels;
-//   single one CTA, 128 tokens x BN channels (128 or 64);
+//   single one CTA, 128 tokens x 32 .. 256 channels (a multiple of 16);
 //   split  `single` with a cluster of up to 8 CTAs over the k-blocks of one
 //          tile, whose int32 sums meet through distributed shared memory.
 // Warps: 0 the TMA producer, 1 the tensor-memory owner and MMA issuer, 4-7
@@ -17,6 +17,17 @@
 // tile's products (pair and single are persistent, split is one tile).
 // Every mbarrier wait is bounded; one that runs out records the timeout in
 // the status word, raises the abort flags and the block winds down.
+//
+// What bounds it: with many tokens the tensor cores (2048 tokens, 8192 ->
+// 28672: 295 - 303 us, 3.18 - 3.26 POPS, where the library's 8192^3 product
+// runs at 2.85; 2560 -> 6912: 27.4 us, 2.64 POPS); with up to 128 tokens and
+// large matrices the weights' stream (32 tokens, 8192 -> 28672: 43 us, 5.5
+// TB/s; 2560 -> 128000: 54 us, 6.2 TB/s), which is why the tile width is free:
+// the tiles should come out even over the SMs (448 tiles of 64 or 224 of 128
+// channels for 148 SMs leave a quarter of the time idle, 138 of 208 none);
+// and in between the latency of a tile's k-blocks, which the split shortens.
+// An MMA of one CTA holds the tensor core for about 130 clocks whatever its
+// width, so narrow tiles are only as fast as wide ones.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <algorithm>

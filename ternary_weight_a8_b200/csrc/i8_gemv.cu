@@ -7,13 +7,20 @@
 // so 8 tokens need a tenth of the legacy tensor path's rate and 32 tokens
 // less than half.
 //
-// A block takes 16 weight rows; its warps split the row's 64-byte chunks
-// between them and join their sums in shared memory.  The MMA's k order is
-// free as long as both operands agree on it, so a lane loads 16 consecutive
+// A block takes 16 (or 32) weight rows; its warps split the rows' 64-byte
+// chunks between them and join their sums in shared memory.  The MMA's k order
+// is free as long as both operands agree on it, so a lane loads 16 consecutive
 // bytes of row g and of row g + 8 (g = lane / 4, 16 bytes at 16 * (lane % 4)
 // of the chunk) and uses their words as the fragments of two MMAs; a token's
 // codes are loaded the same way.  Nothing is staged: the loads go from L2 to
-// the fragments, four chunks in flight per warp and four blocks per SM.
+// the fragments, four chunks in flight per warp and four blocks per SM (32-byte
+// loads, which touch half as many lines at a time, were faster on short calls
+// by up to 8% and slower on the long ones by 10 to 20%).
+//
+// Measured: 1 token, 2560 -> 128000: 52 - 55 us (5.9 - 6.3 TB/s, 90 - 97% of
+// the copy rate by box); 8 tokens, 8192 -> 28672: 36.6 - 38.7 us (93 - 98%);
+// short calls are latency: 1 token, 2560 -> 6912: 5.1 us, of which the weights
+// need 2.7 and an empty launch 2.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

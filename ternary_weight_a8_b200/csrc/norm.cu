@@ -16,7 +16,13 @@
 // dz is the gradient of x and of the residual alike.
 //
 // Both are bound by memory: 7 bytes per bf16 input forward (x, residual, z,
-// codes), 8 backward (z, dv, dz_in, dz).
+// codes), 8 backward (z, dv, dz_in, dz; 10 with fp32 dv).  To get there the
+// arithmetic has to stay small: sums in bf16 pairs, packed fp32 products,
+// maxima as integers, codes by an addition, 1 / rms by Newton's method.
+// 8192 x 8192 bf16 forward took 126 us in scalar arithmetic and takes 78 (91%
+// of the copy rate); backward 167 us, and 93 - 95 (86 - 88%).  2048 x 2560
+// (one wave, 5.6 us of traffic) takes 10.9 us forward and 16.1 backward, of
+// which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -474,11 +480,12 @@ __device__ __forceinline__ void copy_async_wait() {
 
 // The ring of the backward's z and dv: for every stage and chunk, a piece of
 // each thread after the other.  Three stages: a token's output, the next
-// one's sums and the one after on its way.
+// one's sums and the one after on its way; two with fp32 gradients of bf16
+// tokens, whose pieces are half as large again, so that more blocks fit.
 template <typename T, typename TD>
 struct BackRing {
   static constexpr int kZ = 16, kD = kPer<T> * static_cast<int>(sizeof(TD)), kChunk = kZ + kD;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = kChunk > 32 ? 2 : 3;
   static constexpr int bytes(int threads, int chunks) { return kStages * chunks * threads * kChunk; }
 };
 
@@ -622,7 +629,7 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
   int parity = 0, s = 0;
   for (int m = g0; m < P.M; m += stride, parity ^= 1) {
     const size_t row = static_cast<size_t>(m) * P.K;
-    const int s1 = s == 2 ? 0 : s + 1, s2 = s1 == 2 ? 0 : s1 + 1;
+    const int s1 = s == R::kStages - 1 ? 0 : s + 1, s2 = s1 == R::kStages - 1 ? 0 : s1 + 1;
     uint4 in[C];
     if (P.dz_in) {
 #pragma unroll
@@ -632,8 +639,12 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
           in[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.dz_in) + row) + c);
       }
     }
-    request(m + 2 * stride, s2);  // the stage of the token before: this thread has used all it read there
-    copy_async_wait<1>();
+    if constexpr (R::kStages == 3) {
+      request(m + 2 * stride, s2);  // the stage of the token before: this thread has used all it read there
+      copy_async_wait<1>();
+    } else {
+      copy_async_wait<0>();
+    }
     // The next token's sums, posted a whole token ahead of their use.
     f32x2 next = 0;
     if (m + stride < P.M) next = sums_of(s1);
@@ -695,6 +706,7 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
         out[c] = from_pairs<T>(o);
       }
     }
+    if constexpr (R::kStages == 2) request(m + 2 * stride, s);
     if (W > 1) group_sync(bar, 32 * W);
     s = s1;
   }
@@ -853,7 +865,7 @@ __global__ void __launch_bounds__(1024) gain_grad_finish_kernel(const float* __r
   }
 }
 
-constexpr int kRingMax = 220 * 1024;  // of an SM's shared memory
+constexpr int kRingMax = 224 * 1024;  // of a block's shared memory
 
 // How the backward splits its work: from the sizes and the SM count alone, so
 // the workspace figure and the launch agree.
@@ -870,7 +882,7 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   p.W = (chunks + 32 * p.C - 1) / (32 * p.C);
   const int groups = p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
   p.threads = 32 * p.W * groups;
-  const int ring = 3 * p.C * p.threads * piece;
+  const int ring = (piece > 32 ? 2 : 3) * p.C * p.threads * piece;
   if (p.W > kMaxGroupWarps || ring > kRingMax) {
     p.C = 0;
     p.W = kMaxGroupWarps;
@@ -882,7 +894,7 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   // What the registers (64, 80 or 128 a thread) and the ring (`piece` bytes a
   // chunk, three stages) let be resident.
   int resident = (p.C == 1 ? 1024 : p.C == 2 ? 768 : 512) / p.threads;
-  const int by_ring = kRingMax / (ring + 1024) + (ring + 1024 > kRingMax);
+  const int by_ring = 228 * 1024 / (ring + 2048);  // a block's fixed share and its other shared memory
   if (resident > by_ring) resident = by_ring;
   const int need = (M + groups - 1) / groups;
   p.grid = need < resident * sms ? need : resident * sms;
