@@ -265,12 +265,12 @@ class _Call:
     the caller's tensors are recorded on it when it is not the current one, so
     that the allocator gives none of them away too early."""
 
-    __slots__ = ("like", "index", "stream", "handle", "switch", "held")
+    __slots__ = ("device", "index", "stream", "handle", "switch", "held")
 
     def __init__(self, x: torch.Tensor, stream):
         if not x.is_cuda:
             raise ValueError("tensor must be on a CUDA device")
-        self.like = x
+        self.device = x.device
         self.index = x.get_device()
         # The current stream's handle without making a Stream object (2 us of a 15 us call).
         self.handle = torch._C._cuda_getCurrentRawStream(self.index)
@@ -290,7 +290,7 @@ class _Call:
                 and (dtype is None or t.dtype is dtype) and self.stream is None):
             return t.data_ptr()
         if t.get_device() != self.index:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, self.like.device))
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, self.device))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
         if shape is not None and t.shape != shape:
@@ -305,12 +305,11 @@ class _Call:
         """An output of the call, from its stream's memory."""
         if self.stream is None:
             if zero:
-                return self.like.new_zeros(shape, dtype=dtype)
-            if shape == self.like.shape:
-                return torch.empty_like(self.like, dtype=dtype)  # the cheapest of torch's ways
-            return self.like.new_empty(shape, dtype=dtype)
+                return torch.zeros(shape, dtype=dtype, device=self.device)
+            # With its strides said, the cheapest of torch's ways (1.5 us, 2.1 without).
+            return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
-            t = self.like.new_zeros(shape, dtype=dtype) if zero else self.like.new_empty(shape, dtype=dtype)
+            t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.device)
         t.record_stream(torch.cuda.current_stream(self.index))  # the caller may use it there
         return t
 
@@ -340,16 +339,18 @@ class _Call:
             ws = cache.get(key)
             if ws is None or ws.numel() < nbytes:
                 with torch.cuda.stream(self.stream or torch.cuda.current_stream(self.index)):
-                    ws = cache[key] = new_workspace(nbytes, self.like.device)
+                    ws = cache[key] = new_workspace(nbytes, self.device)
         self.held = ws  # until the launches are made
         return ws.data_ptr(), ws.numel()
 
-    def run(self, fn, *args) -> None:
+    def on_device(self, fn, *args):
         if self.switch:
             with torch.cuda.device(self.index):
-                _check(fn(*args, self.handle))
-        else:
-            _check(fn(*args, self.handle))
+                return fn(*args)
+        return fn(*args)
+
+    def run(self, fn, *args) -> None:
+        _check(self.on_device(fn, *args, self.handle))
 
 
 def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, gain: torch.Tensor | None = None, eps: float = 1e-6,
@@ -394,7 +395,7 @@ def add_rmsnorm_backward(z: torch.Tensor, dnorm: torch.Tensor, gain: torch.Tenso
         dgain = None
     if dgain is not None:
         dgain, gp = c.out(None if dgain is True else dgain, "dgain", (K,), torch.float32)
-        wp, nbytes = c.workspace(workspace, lib().bitlinear_add_rmsnorm_backward_workspace_bytes(M, K, code))
+        wp, nbytes = c.workspace(workspace, c.on_device(lib().bitlinear_add_rmsnorm_backward_workspace_bytes, M, K, code))
     c.run(lib().bitlinear_add_rmsnorm_backward, c.ptr(z, "z"), code, c.ptr(dnorm, "dnorm", (M, K)), dcode, M, K,
           c.ptr(gain, "gain", (K,), torch.float32), float(eps), c.ptr(dz_in, "dz_in", (M, K), z.dtype), op, gp, wp,
           nbytes)

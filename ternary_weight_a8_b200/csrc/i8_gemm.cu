@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) i8_gemm_kernel(const __grid_constant
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
+      griddep_wait();  // so that the bounded waits below begin when the copies do
       int tc = 0, s = 0;
       uint32_t ph = 0;
       bool ok = true, issued = false;

@@ -98,12 +98,13 @@ struct AddNormParams {
   double inv_k;
 };
 
-// kFull: the token's chunks are exactly the threads' (no bounds to test, and
-// the chunks' instructions interleave).  C: 16-byte chunks of a token per thread, held in registers from the sum to
+// C: 16-byte chunks of a token per thread, held in registers from the sum to
 // the codes (z's chunk is overwritten by v's).  C = 0: the token is longer
 // than the registers hold, and its chunks wait in shared memory (`staged`), or,
 // longer than that too, z is read back for the absmax and again for the
-// codes; either way each thread reads only what it wrote.
+// codes; either way each thread reads only what it wrote.  kFull: every thread
+// has all its chunks, so their instructions interleave without bounds between
+// them (2048 x 2560 fp32 16.7 -> 14.6 us).
 template <typename T, int C, bool kFull>
 __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
                                                                                          int staged) {
@@ -313,12 +314,12 @@ cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stre
   const dim3 grid((P.M + groups - 1) / groups);
   const int held = n <= 2 ? n : 4;
   const bool full = chunks == held * 32 * W;  // every thread holds as many chunks as it has room for
-  if (n <= 1) return full ? launch(add_rmsnorm_quant_kernel<T, 1, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
-                : launch(add_rmsnorm_quant_kernel<T, 1, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
-  if (n <= 2) return full ? launch(add_rmsnorm_quant_kernel<T, 2, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
-                : launch(add_rmsnorm_quant_kernel<T, 2, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
-  if (n <= 4) return full ? launch(add_rmsnorm_quant_kernel<T, 4, true>, grid, dim3(threads), 0, stream, pdl, P, W, 0)
-                : launch(add_rmsnorm_quant_kernel<T, 4, false>, grid, dim3(threads), 0, stream, pdl, P, W, 0);
+  auto run = [&](auto with_bounds, auto without) {
+    return launch(full ? without : with_bounds, grid, dim3(threads), 0, stream, pdl, P, W, 0);
+  };
+  if (n <= 1) return run(add_rmsnorm_quant_kernel<T, 1, false>, add_rmsnorm_quant_kernel<T, 1, true>);
+  if (n <= 2) return run(add_rmsnorm_quant_kernel<T, 2, false>, add_rmsnorm_quant_kernel<T, 2, true>);
+  if (n <= 4) return run(add_rmsnorm_quant_kernel<T, 4, false>, add_rmsnorm_quant_kernel<T, 4, true>);
   const size_t row = static_cast<size_t>(P.K) * sizeof(T);
   const bool staged = row <= kMaxRowBytes;
   static std::atomic<uint64_t> attr_done{0};
@@ -512,8 +513,9 @@ __device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
 }
 
 // A group of W warps takes tokens group0, group0 + groups_total, ...; a
-// thread owns the same C chunks of every token (kFull: all of them exist), so the gain's gradient is
-// summed in its registers and written once per block.  The two sums over a
+// thread owns the same C chunks of every token (kFull: all of them exist), so
+// the gain's gradient is summed in its registers and written once per block.
+// The two sums over a
 // token run as one pair of fp32 (trees of at most 26 steps): at 16 warps a
 // token, sums and 1 / rms in double were half of the kernel's instructions.
 // z and dv of the next tokens are under way in shared memory, where a thread
@@ -521,7 +523,8 @@ __device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
 // are taken while the token before is written, so that the reduction's chain
 // of shuffles and its barrier wait for nobody.
 template <typename T, typename TD, int C, bool kGain, bool kFull>
-__global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 1) add_rmsnorm_backward_kernel(const AddNormBackParams P, int W) {
+__global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 1)
+    add_rmsnorm_backward_kernel(const AddNormBackParams P, int W) {
   constexpr int N = kPer<T>, NP = kPairs<T>;
   using R = BackRing<T, TD>;
   extern __shared__ uint4 ring[];
@@ -881,8 +884,7 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   p.C = chunks <= 32 ? 1 : chunks <= 512 ? 2 : 4;
   p.W = (chunks + 32 * p.C - 1) / (32 * p.C);
   const int groups = p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
-  p.threads = 32 * p.W * groups;
-  const int ring = (piece > 32 ? 2 : 3) * p.C * p.threads * piece;
+  const long long ring = (piece > 32 ? 2LL : 3LL) * p.C * 32 * p.W * groups * piece;
   if (p.W > kMaxGroupWarps || ring > kRingMax) {
     p.C = 0;
     p.W = kMaxGroupWarps;
@@ -891,10 +893,11 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
     p.rows = M < 64 ? M : 64;
     return p;
   }
+  p.threads = 32 * p.W * groups;
   // What the registers (64, 80 or 128 a thread) and the ring (`piece` bytes a
-  // chunk, three stages) let be resident.
+  // chunk, two or three stages) let be resident.
   int resident = (p.C == 1 ? 1024 : p.C == 2 ? 768 : 512) / p.threads;
-  const int by_ring = 228 * 1024 / (ring + 2048);  // a block's fixed share and its other shared memory
+  const int by_ring = static_cast<int>(228 * 1024 / (ring + 2048));  // a block's fixed share and its other shared memory
   if (resident > by_ring) resident = by_ring;
   const int need = (M + groups - 1) / groups;
   p.grid = need < resident * sms ? need : resident * sms;
