@@ -229,6 +229,33 @@ def test_streams_threads_and_graphs(M):
     assert torch.equal(graphs[0][1], want[0]) and torch.equal(graphs[1][1], want[1])
 
 
+@pytest.mark.parametrize("M", [2, 12, 40, 300])
+def test_weight_offsets_past_32_bits(M):
+    """Weights of more than 2^31 bytes: the first, middle and last channels as calls of their own give them."""
+    N, K = 262144 + 37, 8192
+    w = torch.empty((N, K), dtype=torch.int8, device="cuda")
+    for i in range(0, N, 65536):
+        w[i:i + 65536] = torch.randint(-127, 128, (min(65536, N - i), K), dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, device="cuda") + 0.5
+    q, s = _codes(M, K, 5)
+    qd, sd = dev(q), dev(s)
+    y = tb.forward_i8_quantized(w, ws, qd, sd, out_dtype=torch.float32)
+    for at in (slice(0, 50), slice(131060, 131090), slice(N - 70, N)):
+        assert torch.equal(y[:, at], tb.forward_i8_quantized(w[at].contiguous(), ws[at], qd, sd, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("N,dtype", [(65536, torch.bfloat16), (65529, torch.float32)])
+def test_output_offsets_past_32_bits(N, dtype):
+    """More than 2^31 outputs, in boxes and row by row: the first, middle and last tokens."""
+    M, K = 32768 + 41, 64
+    w, ws = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda"), torch.rand(N, device="cuda") + 0.5
+    q = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda")
+    s = torch.rand(M, device="cuda") + 0.5
+    y = tb.forward_i8_quantized(w, ws, q, s, out_dtype=dtype)
+    for at in (slice(0, 9), slice(16380, 16390), slice(M - 60, M)):
+        assert torch.equal(y[at], tb.forward_i8_quantized(w, ws, q[at].contiguous(), s[at].contiguous(), out_dtype=dtype))
+
+
 def test_refusals():
     w, ws = torch.zeros((64, 128), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
     q, s = torch.zeros((4, 128), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")

@@ -320,6 +320,24 @@ def test_streams_threads_and_graphs():
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last tokens as a call of their own gives them, the first ones too."""
+    M, K = 262144 + 5, 8192
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, M, 65536):
+        x[i:i + 65536] = torch.randn((min(65536, M - i), K), device="cuda")
+    g = dev(_gain(K, 1))
+    z, q, s, r = tb.add_rmsnorm_quant(x, x, g)
+    dz, dg = tb.add_rmsnorm_backward(z, x, g, dz_in=x)
+    assert torch.isfinite(dg).all()
+    for at in (slice(0, 7), slice(131068, 131077), slice(M - 7, M)):
+        part = x[at].contiguous()
+        z2, q2, s2, r2 = tb.add_rmsnorm_quant(part, part, g)
+        assert torch.equal(z[at], z2) and torch.equal(q[at], q2) and torch.equal(s[at], s2) and torch.equal(r[at], r2)
+        assert torch.equal(dz[at], tb.add_rmsnorm_backward(z2, part, g, dz_in=part, dgain=False)[0])
+
+
+@pytest.mark.gpu
 def test_refusals():
     x = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
     f = torch.zeros((4, 128), device="cuda")
