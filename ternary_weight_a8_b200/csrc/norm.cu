@@ -25,6 +25,8 @@
 // which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "pairs.cuh"
@@ -505,6 +507,18 @@ __device__ __forceinline__ void store_pairs(float* p, const f32x2 (&v)[P2]) {
 // overflow above 2^128 and lose bits below 2^-126).
 constexpr float kSquaresLow = 1e-25f, kSquaresHigh = 1e37f;
 
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ void st_cluster_b64(uint32_t cluster_addr, f32x2 v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive_release() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_acquire() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // The two sums of a pair over the warp, in one butterfly.
 __device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
 #pragma unroll
@@ -518,25 +532,52 @@ __device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
 // The two sums over a
 // token run as one pair of fp32 (trees of at most 26 steps): at 16 warps a
 // token, sums and 1 / rms in double were half of the kernel's instructions.
-// z and dv of the next tokens are under way in shared memory, where a thread
-// reads only what it copied itself, so no barrier guards them; a token's sums
-// are taken while the token before is written, so that the reduction's chain
-// of shuffles and its barrier wait for nobody.
-template <typename T, typename TD, int C, bool kGain, bool kFull>
+// A token of more than 1024 chunks is shared by a cluster (kCluster: C chunks
+// of 32 W threads in each of its CTAs), whose sums meet in every CTA's shared
+// memory.  z and dv of the next tokens are under way in shared memory, where a
+// thread reads only what it copied itself, so no barrier guards them; a
+// token's sums are taken while the token before is written, so that the
+// reduction's chain of shuffles and its barrier wait for nobody.
+template <typename T, typename TD, int C, bool kGain, bool kFull, bool kCluster>
 __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 1)
     add_rmsnorm_backward_kernel(const AddNormBackParams P, int W) {
   constexpr int N = kPer<T>, NP = kPairs<T>;
   using R = BackRing<T, TD>;
   extern __shared__ uint4 ring[];
-  __shared__ f32x2 red[2][kMaxGroupWarps];
-  __shared__ double red_d[kMaxGroupWarps];
+  constexpr int kSlots = kCluster ? kMaxGroupWarps * kMaxCluster : kMaxGroupWarps;
+  __shared__ f32x2 red[2][kSlots];
+  __shared__ double red_d[kSlots];
   griddep_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / W, wig = warp % W, groups = (blockDim.x >> 5) / W;
-  const int g0 = blockIdx.x * groups + group, stride = gridDim.x * groups;
-  const int tid = wig * 32 + lane, step = 32 * W, chunks = P.K / N, bar = 1 + group;
+  const int cl = kCluster ? static_cast<int>(cluster_nctarank()) : 1;
+  const int rank = kCluster ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = kCluster ? 0 : warp / W, wig = kCluster ? warp : warp % W;
+  const int groups = kCluster ? 1 : (blockDim.x >> 5) / W;
+  const int g0 = kCluster ? blockIdx.x / cl : blockIdx.x * groups + group;
+  const int stride = kCluster ? gridDim.x / cl : gridDim.x * groups;
+  // A thread's chunks are tid, tid + step, ... of its token (of its CTA's part).
+  const int tid = (kCluster ? rank * C * 32 * W : 0) + wig * 32 + lane, step = 32 * W;
+  const int chunks = P.K / N, bar = 1 + group;
+  if constexpr (kCluster) cluster_sync_all();  // the others' shared memory is there
   griddep_wait();
+  // This warp's pair of sums into its place in every CTA of the cluster.
+  auto post = [&](f32x2 (&slots)[kSlots], f32x2 v) {
+    if constexpr (kCluster) {
+      if (lane < cl) st_cluster_b64(mapa_shared(smem_u32(&slots[rank * W + wig]), static_cast<uint32_t>(lane)), v);
+    } else {
+      if (lane == 0) slots[group * W + wig] = v;
+    }
+  };
+  auto total = [&](const f32x2 (&slots)[kSlots]) {
+    f32x2 v = 0;
+    if constexpr (kCluster) {
+      for (int i = lane; i < cl * W; i += 32) v = add2(v, slots[i]);
+    } else {
+      if (lane < W) v = slots[group * W + lane];
+    }
+    return warp_sum2(v);
+  };
 
   // The gains and the sums of their gradient stay in registers: reading 4
   // bytes of gain for every 2 of z, twice a token, kept the kernel waiting.
@@ -625,8 +666,11 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
   copy_async_wait<1>();
   f32x2 both = 0;
   if (g0 < P.M) both = sums_of(0);
-  if (W > 1) {
-    if (lane == 0) red[0][group * W + wig] = both;
+  if constexpr (kCluster) {
+    post(red[0], both);
+    cluster_sync_all();
+  } else if (W > 1) {
+    post(red[0], both);
     group_sync(bar, 32 * W);
   }
   int parity = 0, s = 0;
@@ -651,9 +695,9 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
     // The next token's sums, posted a whole token ahead of their use.
     f32x2 next = 0;
     if (m + stride < P.M) next = sums_of(s1);
-    if (W > 1) {
-      if (lane == 0) red[parity ^ 1][group * W + wig] = next;
-      both = warp_sum2(lane < W ? red[parity][group * W + lane] : 0);
+    if (kCluster || W > 1) {
+      post(red[parity ^ 1], next);
+      both = total(red[parity]);
     }
     float ss, dot;
     split2(both, ss, dot);
@@ -675,10 +719,25 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
           }
         }
       }
-      if (W > 1) group_sync(bar, 32 * W);  // red_d may still be read for an earlier token
-      t = group_reduce(t, [](double a, double b) { return __dadd_rn(a, b); }, red_d + group * W, W, wig, lane, bar);
+      auto add = [](double a, double b) { return __dadd_rn(a, b); };
+      if constexpr (kCluster) {
+        cluster_sync_all();  // red_d may still be read for an earlier token
+        t = warp_reduce(t, add);
+        if (lane < cl)
+          st_cluster_b64(mapa_shared(smem_u32(&red_d[rank * W + wig]), static_cast<uint32_t>(lane)),
+                         static_cast<f32x2>(__double_as_longlong(t)));
+        cluster_sync_all();
+        t = red_d[0];
+        for (int i = 1; i < cl * W; ++i) t = add(t, red_d[i]);
+      } else {
+        if (W > 1) group_sync(bar, 32 * W);  // red_d may still be read for an earlier token
+        t = group_reduce(t, add, red_d + group * W, W, wig, lane, bar);
+      }
       r = rstd_of(t, P.K, P.inv_k, P.eps);
     }
+    // This token's sums are read and the next one's posted: the barrier may
+    // begin, and is waited for once the token is written.
+    if constexpr (kCluster) cluster_arrive_release();
     const float mean = dot * r * P.inv_kf;
     const f32x2 r2 = pack2(r, r), mean2 = pack2(-mean, -mean);
     uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row);
@@ -710,13 +769,17 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
       }
     }
     if constexpr (R::kStages == 2) request(m + 2 * stride, s);
-    if (W > 1) group_sync(bar, 32 * W);
+    if constexpr (kCluster) {
+      cluster_wait_acquire();
+    } else if (W > 1) {
+      group_sync(bar, 32 * W);
+    }
     s = s1;
   }
   if constexpr (kGain) {
     if (P.part) {
       // One row of sums per block: its groups' rows meet in the ring, in order.
-      float* out = P.part + static_cast<size_t>(blockIdx.x) * P.K;
+      float* out = P.part + static_cast<size_t>(kCluster ? g0 : blockIdx.x) * P.K;
       float* own = groups > 1 ? reinterpret_cast<float*>(ring) + group * P.K : out;
       if (groups > 1) {
         copy_async_wait<0>();
@@ -739,8 +802,9 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
   }
 }
 
-// Tokens longer than the registers hold: one block per token reads it twice
-// (the second time from L2) and leaves 1 / rms in rstd for the gain's gradient.
+// Tokens longer than a cluster holds (131072 bf16 inputs, 65536 fp32): one
+// block per token reads it twice (the second time from L2) and leaves 1 / rms
+// in rstd for the gain's gradient.
 template <typename T, typename TD>
 __global__ void __launch_bounds__(512, 2) add_rmsnorm_backward_long_kernel(const AddNormBackParams P) {
   constexpr int N = kPer<T>, NP = kPairs<T>;
@@ -874,6 +938,7 @@ constexpr int kRingMax = 224 * 1024;  // of a block's shared memory
 // the workspace figure and the launch agree.
 struct BackPlan {
   int W, C, threads, grid, rows;  // C = 0: the long form; rows of the partial gain gradient
+  int cluster;                    // CTAs per token
 };
 
 BackPlan plan_backward(int M, int K, int per, int piece) {
@@ -882,11 +947,22 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   const int sms = num_sms();
   // Chunks per thread: one while a warp holds the token, two while eight do, else four.
   p.C = chunks <= 32 ? 1 : chunks <= 512 ? 2 : 4;
-  p.W = (chunks + 32 * p.C - 1) / (32 * p.C);
-  const int groups = p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
+  // Longer than eight warps of four chunks hold: a cluster of such blocks (512
+  // tokens of 28672: 35 us bf16, 57 fp32; read twice by one block each and a
+  // third time for the gain 44 and 80; 1024 bf16 tokens of 8640 with fp32
+  // gradients 29.5 us, 31.3 in one block of nine warps), or of blocks of up to
+  // sixteen warps where eight CTAs are too few.
+  p.cluster = 1;
+  if (chunks > 4 * kNormThreads) {
+    p.cluster = (chunks - 1) / (4 * kNormThreads) + 1;
+    if (p.cluster > kMaxCluster) p.cluster = (chunks - 1) / (32 * 4 * kMaxGroupWarps) + 1;
+  }
+  p.W = (chunks - 1) / (32 * p.C * p.cluster) + 1;
+  const int groups = p.cluster > 1 || p.W > kNormThreads / 32 ? 1 : kNormThreads / 32 / p.W;
   const long long ring = (piece > 32 ? 2LL : 3LL) * p.C * 32 * p.W * groups * piece;
-  if (p.W > kMaxGroupWarps || ring > kRingMax) {
+  if (p.W > kMaxGroupWarps || p.cluster > kMaxCluster || ring > kRingMax) {
     p.C = 0;
+    p.cluster = 1;
     p.W = kMaxGroupWarps;
     p.threads = 32 * kMaxGroupWarps;
     p.grid = M;
@@ -900,34 +976,51 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   const int by_ring = static_cast<int>(228 * 1024 / (ring + 2048));  // a block's fixed share and its other shared memory
   if (resident > by_ring) resident = by_ring;
   const int need = (M + groups - 1) / groups;
-  p.grid = need < resident * sms ? need : resident * sms;
-  p.rows = p.grid;
+  int most = resident * sms;
+  // Clusters do not use every SM: the SMs of one share a GPC (of 148 SMs, 33
+  // clusters of four fit and 28 of five do not).
+  if (p.cluster > 1) most = std::max(1, most / p.cluster * (p.cluster > 2 ? 7 : 8) / 8);
+  p.rows = need < most ? need : most;
+  p.grid = p.rows * p.cluster;
   return p;
 }
 
-template <typename T, typename TD, int C, bool kGain, bool kFull>
+template <typename T, typename TD, int C, bool kGain, bool kFull, bool kCluster>
 cudaError_t launch_back_k(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
+  auto kernel = add_rmsnorm_backward_kernel<T, TD, C, kGain, kFull, kCluster>;
   static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(add_rmsnorm_backward_kernel<T, TD, C, kGain, kFull>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMax);
-  });
+  const cudaError_t e = once_per_device(
+      attr_done, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMax); });
   if (e != cudaSuccess) return e;
-  return launch(add_rmsnorm_backward_kernel<T, TD, C, kGain, kFull>, dim3(p.grid), dim3(p.threads),
-                BackRing<T, TD>::bytes(p.threads, C), stream, true, P, p.W);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid);
+  cfg.blockDim = dim3(p.threads);
+  cfg.dynamicSmemBytes = BackRing<T, TD>::bytes(p.threads, C);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P, p.W);
 }
 
 template <typename T, typename TD, bool kGain, bool kFull>
 cudaError_t launch_back_f(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
-  if (p.C == 1) return launch_back_k<T, TD, 1, kGain, kFull>(P, p, stream);
-  if (p.C == 2) return launch_back_k<T, TD, 2, kGain, kFull>(P, p, stream);
-  return launch_back_k<T, TD, 4, kGain, kFull>(P, p, stream);
+  if (p.cluster > 1) return launch_back_k<T, TD, 4, kGain, kFull, true>(P, p, stream);
+  if (p.C == 1) return launch_back_k<T, TD, 1, kGain, kFull, false>(P, p, stream);
+  if (p.C == 2) return launch_back_k<T, TD, 2, kGain, kFull, false>(P, p, stream);
+  return launch_back_k<T, TD, 4, kGain, kFull, false>(P, p, stream);
 }
 
 template <typename T, typename TD, bool kGain>
 cudaError_t launch_back_c(const AddNormBackParams& P, const BackPlan& p, cudaStream_t stream) {
-  return P.K / kPer<T> == p.C * 32 * p.W ? launch_back_f<T, TD, kGain, true>(P, p, stream)
-                                         : launch_back_f<T, TD, kGain, false>(P, p, stream);
+  return P.K / kPer<T> == p.C * 32 * p.W * p.cluster ? launch_back_f<T, TD, kGain, true>(P, p, stream)
+                                                     : launch_back_f<T, TD, kGain, false>(P, p, stream);
 }
 
 template <typename T, typename TD>
