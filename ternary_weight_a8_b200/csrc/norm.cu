@@ -950,10 +950,13 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   // Longer than eight warps of four chunks hold: a cluster of such blocks (512
   // tokens of 28672: 35 us bf16, 57 fp32; read twice by one block each and a
   // third time for the gain 44 and 80; 1024 bf16 tokens of 8640 with fp32
-  // gradients 29.5 us, 31.3 in one block of nine warps), or of blocks of up to
-  // sixteen warps where eight CTAs are too few.
+  // gradients 29.5 us, 31.3 in one block of nine warps), unless 12 or 16 warps
+  // hold it, an even share for an SM's four schedulers (4096 fp32 tokens of
+  // 8192: 88.5 us, 91.8 in clusters of two); or a cluster of up to sixteen
+  // warps where eight CTAs of eight are too few.
   p.cluster = 1;
-  if (chunks > 4 * kNormThreads) {
+  const int warps = (chunks - 1) / (32 * 4) + 1;
+  if (warps > kNormThreads / 32 && (warps > kMaxGroupWarps || warps % 4 != 0)) {
     p.cluster = (chunks - 1) / (4 * kNormThreads) + 1;
     if (p.cluster > kMaxCluster) p.cluster = (chunks - 1) / (32 * 4 * kMaxGroupWarps) + 1;
   }
