@@ -7,6 +7,7 @@ a norm and a BitLinear there and back.
 """
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -112,6 +113,46 @@ def test_norm_and_layer_backward(M, K, N):
     assert (np.abs(dz.float().cpu().numpy() - want) <= bar).all()
     wg = (d64 * n).sum(0)
     assert (np.abs(dgain.cpu().numpy() - wg) <= U * (N + M + 300) * (terms / np.abs(g64) * np.abs(n)).sum(0)).all()
+
+
+def test_all_calls_at_once_on_two_streams():
+    """Two host threads, each on a stream of its own, every operator in every form at the same time."""
+    sets = []
+    for k in range(2):
+        gen = torch.Generator(device="cuda").manual_seed(k)
+        rnd = lambda *shape: torch.randn(shape, generator=gen, device="cuda")
+        g = rnd(2560) * 0.1 + 1
+        wide = rnd(40960) * 0.1 + 1
+        wq, ws = tb.quant_weights_i8(rnd(6912, 2560))
+        x = {m: rnd(m, 2560).bfloat16() for m in (1, 12, 47, 129, 700)}
+        long = rnd(9, 40960)
+
+        def calls(x=x, g=g, wide=wide, wq=wq, ws=ws, long=long):
+            out = []
+            for v in x.values():
+                out.append(tb.forward_i8(wq, ws, v))
+                z, q, s, r = tb.add_rmsnorm_quant(v, v, g)
+                out += [z, q, s, r, tb.forward_i8_quantized(wq, ws, q, s, out_dtype=torch.float32)]
+                out += tb.add_rmsnorm_backward(z, v, g, dz_in=v)
+            out += tb.add_rmsnorm_backward(long, long, wide)
+            out += tb.add_rmsnorm_quant(long, long, wide)
+            return out
+        sets.append((calls, calls()))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        calls, want = sets[k]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(15):
+                got = calls()
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad
 
 
 def test_first_calls_inside_a_capture():
