@@ -13,15 +13,16 @@
 // bytes of row g and of row g + 8 (g = lane / 4, 16 bytes at 16 * (lane % 4)
 // of the chunk) and uses their words as the fragments of two MMAs; a token's
 // codes are loaded the same way.  Nothing is staged: the loads go from L2 to
-// the fragments, four chunks in flight per warp and four blocks per SM (32-byte
-// loads, which touch half as many lines at a time, were faster on short calls
-// by up to 8% and slower on the long ones by 10 to 20%).
+// the fragments, a batch of U chunks in flight per warp and BPS blocks per SM
+// (32-byte loads, which touch half as many lines at a time, were faster on
+// short calls by up to 8% and slower on the long ones by 10 to 20%).
 //
-// Measured: 1 token, 2560 -> 128000: 52 - 55 us (5.9 - 6.3 TB/s, 90 - 97% of
-// the copy rate by box); 8 tokens, 8192 -> 28672: 36.6 - 38.7 us (93 - 98%);
-// short calls are latency: 1 token, 2560 -> 6912: 5.1 us, of which the weights
-// need 2.7 and an empty launch 2.
+// Measured, the weights new in every call: 1 token, 2560 -> 128000: 51.3 us
+// (6.4 TB/s, 97% of the copy rate); 8 tokens, 8192 -> 28672: 38.4 us (93%);
+// 1 token, 28672 -> 8192: 37.3 us; short calls are latency: 1 token, 2560 ->
+// 6912: 4.9 us, of which the weights need 2.7 and an empty launch 2.
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -104,8 +105,8 @@ __device__ __forceinline__ void block_codes(const I8Args& P, int8_t* codes, int 
 // TG: groups of 8 tokens; MT: groups of 16 rows; U: chunks in flight per warp.
 // TX: the type of raw tokens that the block quantises itself, or int8_t for
 // codes.
-template <typename TX, typename TY, int TG, int MT, int U0>
-__global__ void __launch_bounds__(32 * kGvWarps, sizeof(TX) > 1 || TG * MT >= 4 ? 3 : 4)
+template <typename TX, typename TY, int TG, int MT, int U, int BPS>
+__global__ void __launch_bounds__(32 * kGvWarps, BPS)
     i8_gemv_kernel(const I8Args P, int first_wave) {
   constexpr bool kRaw = sizeof(TX) > 1;
   constexpr int kRows = 16 * MT;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(32 * kGvWarps, sizeof(TX) > 1 || TG * MT >= 4 
                      : "memory");
     } else {
 #pragma unroll
-      for (int u = 0; u < U0; ++u)
+      for (int u = 0; u < U; ++u)
         if (c0 + u < c1) {
 #pragma unroll
           for (int i = 0; i < 2 * MT; ++i) prefetch_l2(wp[i] + 64 * (c0 + u));
@@ -152,20 +153,32 @@ __global__ void __launch_bounds__(32 * kGvWarps, sizeof(TX) > 1 || TG * MT >= 4 
   griddep_wait();
 
   int acc[MT][TG][4] = {};
-  auto fetch = [&](int c, auto& a, auto n_tag) {
-    constexpr int U = decltype(n_tag)::value;
+  // A batch of U chunks, all in flight together; the last one is cut at c1
+  // (what it lacks is zero), since chunks one by one would each wait alone.
+  auto fetch = [&](int c, uint4 (&a)[U][2 * MT], auto cut) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) a[u][i] = ldg_stream_u4(wp[i] + 64 * (c + u));
+      for (int i = 0; i < 2 * MT; ++i) {
+        if (!decltype(cut)::value || c + u < c1) {
+          a[u][i] = ldg_stream_u4(wp[i] + 64 * (c + u));
+        } else {
+          a[u][i] = make_uint4(0, 0, 0, 0);
+        }
+      }
   };
-  auto use = [&](int c, auto& a, auto n_tag) {
-    constexpr int U = decltype(n_tag)::value;
+  auto use = [&](int c, uint4 (&a)[U][2 * MT], auto cut) {
     uint4 x[U][TG];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < TG; ++j) x[u][j] = *reinterpret_cast<const uint4*>(xp[j] + 64 * (c + u));
+      for (int j = 0; j < TG; ++j) {
+        if (!decltype(cut)::value || c + u < c1) {
+          x[u][j] = *reinterpret_cast<const uint4*>(xp[j] + 64 * (c + u));
+        } else {
+          x[u][j] = make_uint4(0, 0, 0, 0);
+        }
+      }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -177,31 +190,27 @@ __global__ void __launch_bounds__(32 * kGvWarps, sizeof(TX) > 1 || TG * MT >= 4 
           mma_s8(acc[i][j], lo.z, hi.z, lo.w, hi.w, x[u][j].z, x[u][j].w);
         }
   };
-  const std::integral_constant<int, U0> full{};
-  const std::integral_constant<int, 1> one{};
+  const std::true_type cut{};
+  const std::false_type whole{};
   int c = c0;
   if constexpr (kRaw) {
     // The first weights are under way while the block quantises.
-    uint4 first[U0][2 * MT];
-    const bool some = c0 + U0 <= c1;
-    if (some) fetch(c0, first, full);
+    uint4 first[U][2 * MT];
+    fetch(c0, first, cut);
     block_codes<TX>(P, reinterpret_cast<int8_t*>(raw_codes), pitch, raw_scales);
-    if (some) {
-      use(c0, first, full);
-      c += U0;
-    }
+    use(c0, first, cut);
+    c += U;
   }
-  for (; c + U0 <= c1; c += U0) {
-    uint4 a[U0][2 * MT];
-    fetch(c, a, full);
-    use(c, a, full);
+  for (; c + U <= c1; c += U) {
+    uint4 a[U][2 * MT];
+    fetch(c, a, whole);
+    use(c, a, whole);
   }
-  if constexpr (U0 > 1)
-    for (; c < c1; ++c) {
-      uint4 a[1][2 * MT];
-      fetch(c, a, one);
-      use(c, a, one);
-    }
+  if (c < c1) {
+    uint4 a[U][2 * MT];
+    fetch(c, a, cut);
+    use(c, a, cut);
+  }
 
   __syncthreads();  // the sums are zero
   // Fragment (row g or g + 8, tokens 2t and 2t + 1) of every group; integer
@@ -231,54 +240,95 @@ __global__ void __launch_bounds__(32 * kGvWarps, sizeof(TX) > 1 || TG * MT >= 4 
   }
 }
 
-template <typename TX, typename TY, int TG, int MT, int U>
+template <typename TX, typename TY, int TG, int MT, int U, int BPS>
 cudaError_t launch_k(const I8Args& a, cudaStream_t stream, bool pdl) {
   const int blocks = (a.N + 16 * MT - 1) / (16 * MT);
-  const int resident = (sizeof(TX) > 1 || TG * MT >= 4 ? 3 : 4) * num_sms();
-  // Blocks whose first weights are fetched into L2 ahead.  Where the grid is
-  // one wave of more than two blocks per SM and nothing has to be quantised
-  // first, the extra requests cost more than they hide (1 token, 2560 -> 6912:
-  // 5.1 us without, 5.3 with; 2560 -> 2560: 3.8 and 3.6; 2560 -> 128000: 56.2
-  // and 54.2, or 70 when later waves fetch ahead too).
+  const int resident = BPS * num_sms();
+  // Blocks whose first weights are fetched into L2 ahead: the first wave of
+  // several (1 token, 8192 -> 28672: 37.1 us, 38.2 without; 2560 -> 32000: 15.9
+  // and 16.8), never more (2560 -> 128000: 70 us, 52).  Where all blocks are
+  // resident they fetch at up to two per SM (1024 -> 4096: 2.2 us, 2.8 without;
+  // 28672 -> 4096: 19.5 and 20.8), not at more (2560 -> 6912: 5.0 and 4.9) nor
+  // for more than 8 tokens, whose codes share L2 (16 tokens, 4096 -> 4096: 5.8
+  // and 5.0), unless they have to quantise first, which gives the time.
   constexpr bool kRaw = sizeof(TX) > 1;
-  const int wave = blocks > resident ? resident : kRaw || blocks <= 2 * num_sms() ? blocks : 0;
+  const int wave = blocks > resident ? resident : kRaw || (TG == 1 && blocks <= 2 * num_sms()) ? blocks : 0;
   const size_t smem = kRaw ? static_cast<size_t>(a.M) * (a.K | 64) : 0;
-  return launch(i8_gemv_kernel<TX, TY, TG, MT, U>, dim3(blocks), dim3(32 * kGvWarps), smem, stream, pdl, a, wave);
+  return launch(i8_gemv_kernel<TX, TY, TG, MT, U, BPS>, dim3(blocks), dim3(32 * kGvWarps), smem, stream, pdl, a, wave);
 }
 
+// The zeros that batches of `u` chunks pad a warp's share of K with.
+inline int padding(int K, int u) {
+  const int share = (K / 64 + kGvWarps - 1) / kGvWarps;
+  return (share + u - 1) / u * u - share;
+}
+
+// Batches of UA chunks, or of UB where those pad less.
+template <typename TX, typename TY, int TG, int UA, int UB, int BPS>
+cudaError_t launch_u(const I8Args& a, cudaStream_t stream, bool pdl) {
+  return padding(a.K, UB) < padding(a.K, UA) ? launch_k<TX, TY, TG, 1, UB, BPS>(a, stream, pdl)
+                                             : launch_k<TX, TY, TG, 1, UA, BPS>(a, stream, pdl);
+}
+
+// A warp waits once per batch, so a batch should be long and its last one full
+// (4 tokens, U = 5 and 8, three blocks per SM: 2560 -> 6912, 5 chunks a warp,
+// 4.9 and 5.1 us; 4096 -> 6912, 8 chunks, 6.4 and 6.3; 3200 -> 6912, 7 chunks,
+// 6.0 and 5.4).  Registers pay for it, so a block takes as many as the grid
+// leaves it: two blocks per SM where no SM gets more (4 tokens, 8192 -> 4096:
+// 7.5 us, 8.7 with three; 16 tokens, 2560 -> 2560: 3.8 with two, 4.8 with
+// three), four where four make one wave (1 token, 28672 -> 8192: 37.3 us, 45
+// with three) and where blocks are many, for their starts and ends (4 tokens,
+// 4096 -> 128000: 78 us, 83 with three; 2560 -> 32000: 16.7 and 16.0).
 template <typename TY>
 cudaError_t launch_i8_gemv_t(const I8Args& a, cudaStream_t stream, bool pdl) {
-  if (a.x) return a.x_bf16 ? launch_k<__nv_bfloat16, TY, 1, 1, 4>(a, stream, pdl) : launch_k<float, TY, 1, 1, 4>(a, stream, pdl);
-  if (a.M <= 8) {
-    // Short rows and enough of them for several waves of twice as large blocks
-    // (1 token, 2560 -> 128000: 51.7 us, 54.7 with 16 rows; 8 tokens, 8192 ->
-    // 28672: 39.5 us, 36.6 with 16 rows; 2560 -> 6912: 6.8 us, 5.3).
-    if (a.K <= 4096 && a.N >= 32 * 8 * num_sms()) return launch_k<int8_t, TY, 1, 2, 2>(a, stream, pdl);
-    return launch_k<int8_t, TY, 1, 1, 4>(a, stream, pdl);
+  using bf16 = __nv_bfloat16;
+  const int per_sm = (a.N + 16 * num_sms() - 1) / (16 * num_sms());
+  if (a.x) {
+    // The first batch stays in registers while the block quantises, beside the
+    // tokens' values, which at three blocks per SM leaves room for four chunks
+    // (1 token, 8192 -> 7000: 11.9 us, 14.1 with five).
+    if (per_sm <= 2)
+      return a.x_bf16 ? launch_k<bf16, TY, 1, 1, 5, 2>(a, stream, pdl) : launch_k<float, TY, 1, 1, 5, 2>(a, stream, pdl);
+    return a.x_bf16 ? launch_u<bf16, TY, 1, 4, 5, 3>(a, stream, pdl) : launch_u<float, TY, 1, 4, 5, 3>(a, stream, pdl);
   }
-  if (a.M <= 16) return launch_k<int8_t, TY, 2, 1, 4>(a, stream, pdl);
-  return launch_k<int8_t, TY, 4, 1, 4>(a, stream, pdl);
+  if (a.M <= 8) {
+    if (per_sm <= 2) return launch_u<int8_t, TY, 1, 5, 8, 2>(a, stream, pdl);
+    if (per_sm != 4 && per_sm <= 15) return launch_u<int8_t, TY, 1, 5, 8, 3>(a, stream, pdl);
+    // Two chunks a warp: twice the rows per block (8 tokens, 1024 -> 128000:
+    // 23.8 us, 28.2 with 16 rows; 1536 -> 128000: 37.4 and 33.0).
+    if (per_sm > 15 && a.K <= 1024) return launch_k<int8_t, TY, 1, 2, 2, 4>(a, stream, pdl);
+    return launch_u<int8_t, TY, 1, 4, 5, 4>(a, stream, pdl);
+  }
+  if (a.M <= 16) {
+    if (per_sm <= 2) return launch_u<int8_t, TY, 2, 5, 8, 2>(a, stream, pdl);
+    if (per_sm <= 3) return launch_u<int8_t, TY, 2, 4, 5, 3>(a, stream, pdl);
+    return launch_k<int8_t, TY, 2, 1, 4, 4>(a, stream, pdl);
+  }
+  // 32 tokens, 2560 -> 2560: 5.3 us with two blocks per SM, 6.5 with three;
+  // 2560 -> 6912: 7.2 with three, 9.8 with two.
+  return per_sm <= 2 ? launch_k<int8_t, TY, 4, 1, 5, 2>(a, stream, pdl) : launch_k<int8_t, TY, 4, 1, 3, 3>(a, stream, pdl);
 }
 
 }  // namespace
 
 // Up to 8 tokens always.  More tokens read as many codes as weights or more
-// through L1, which only a call short enough for its latency to count gains
-// from: 16 tokens, 2560 -> 6912: 5.9 us against 8.7 on the tensor cores, 8640
-// -> 3200: 9.9 against 10.4, 2560 -> 128000: 66 against 55; 32 tokens, 2560
-// -> 6912: 7.1 against 8.7, 8640 -> 3200: 14.0 against 10.4, 8192 -> 28672:
-// 64 against 43.
+// through L1, so the blocks should be one wave, and not of few long rows, which
+// the tensor cores' split of K spreads over more SMs.  16 tokens against the
+// tensor cores: 2560 -> 6912: 5.5 us and 8.3, 8192 -> 8192: 13.3 and 15.8, 4096
+// -> 9472: 8.5 and 11.5, but 2560 -> 12800: 11.9 and 10.5, 16384 -> 2048: 12.5
+// and 11.3.  32 tokens: 2560 -> 6912: 7.2 and 8.7, 4096 -> 6912: 9.4 and 10.8,
+// but 2560 -> 8640: 13.0 and 9.7, 5120 -> 5120: 10.6 and 9.7, 6912 -> 2560:
+// 9.7 and 8.4.
 bool i8_takes_gemv(int M, int N, int K) {
-  const long long weights = static_cast<long long>(N) * K;
-  return M <= 8 || (M <= 16 && weights <= (64LL << 20)) || (M <= kI8GemvMaxTokens && weights <= (20LL << 20));
+  const int per_sm = (N + 16 * num_sms() - 1) / (16 * num_sms());
+  return M <= 8 || (M <= 16 && per_sm <= 4 && K <= 12288) || (M <= kI8GemvMaxTokens && per_sm <= 3 && K <= 4096);
 }
 
 // One wave of blocks can afford to quantise the tokens in every block, when
 // that is short: one or two tokens, or at most the four chunks a thread keeps
-// in registers (1 token, 2560 -> 6912: 6.0 us, 6.6 with a launch for the
-// codes; 8192 -> 2560: 8.3 and 9.7; 4 tokens, 2560 -> 2560: 5 chunks a thread,
-// 5.6 and 5.4; 8 tokens, 2048 -> 4096: 8 chunks, 6.4 and 5.2).  The codes have
-// to fit beside the blocks of an SM.
+// in registers, and not many values (1 token, 2560 -> 6912: 6.1 us, 6.4 with a
+// launch for the codes; 2 tokens, 4096 -> 4096: 6.1 and 6.6; 4 tokens, 2560 ->
+// 2560: 5 chunks a thread, 5.1 and 4.9; 2 tokens, 8192 -> 4096: 10.7 and 9.1).
 bool i8_gemv_quantises(int M, int N, int K, int x_bf16) {
   const int warps = M == 1 ? kGvWarps : M == 2 ? 4 : M <= 4 ? 2 : 1;
   const int chunks = K / (x_bf16 ? 8 : 4);

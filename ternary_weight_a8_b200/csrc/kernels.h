@@ -214,7 +214,7 @@ struct I8Args {
   const void* x = nullptr;
   int x_bf16 = 0;
 };
-constexpr int kI8RawMax = 16384;      // values of raw tokens
+constexpr int kI8RawMax = 8192;       // values of raw tokens
 constexpr int kI8MaxK = 131008;       // 128 * 128 * K < 2^31
 constexpr int kI8GemvMaxTokens = 32;
 bool i8_takes_gemv(int M, int N, int K);                  // the decode kernel's sizes

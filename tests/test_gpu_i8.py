@@ -77,6 +77,31 @@ def test_parity(M, N, K, dtype):
         assert torch.equal(acc2, acc) and torch.equal(y2, y) and torch.equal(y3, y)
 
 
+# 64-byte chunks of a row, which 8 warps share in batches: none for some warps,
+# one each, shares of unequal length, whole batches and batches cut short.
+@pytest.mark.parametrize("chunks", [1, 7, 8, 9, 16, 17, 24, 39, 40, 41, 63, 64, 65, 81, 135])
+def test_decode_batches_and_grids(chunks):
+    K = 64 * chunks
+    gen = torch.Generator("cuda").manual_seed(chunks)
+    w = torch.randint(-128, 128, (38001, K), dtype=torch.int8, device="cuda", generator=gen)
+    ws = torch.rand(38001, device="cuda", generator=gen) + 0.5
+    for M in (1, 8, 16, 31):
+        q = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda", generator=gen)
+        s = torch.rand(M, device="cuda", generator=gen) + 0.5
+        x = torch.randn(M, K, device="cuda", generator=gen)
+        full = (q.double() @ w.double().T).to(torch.int32)  # exact
+        xq, xs, _ = tb.quant_act(x)
+        raw = (xq.double() @ w.double().T).to(torch.int32)
+        # One to five and sixteen blocks of 16 rows per SM, the last one cut.
+        for N in (2361, 4733, 7101, 9470, 11800, 38001):
+            y, acc = tb.forward_i8_quantized(w[:N], ws[:N], q, s, out_dtype=torch.float32, acc_out=True)
+            assert torch.equal(acc, full[:, :N]), (M, N)
+            f = torch.ones_like(s).div(s)[:, None] * torch.ones_like(ws[:N]).div(ws[:N])
+            assert torch.equal(y, full[:, :N].float() * f), (M, N)
+            acc = tb.forward_i8(w[:N], ws[:N], x, acc_out=True)[1]
+            assert torch.equal(acc, raw[:, :N]), (M, N)
+
+
 @pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 32, 40, 300])
 @pytest.mark.parametrize("K", [64, 2048, 2560, 8640, 16384, 16448])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
