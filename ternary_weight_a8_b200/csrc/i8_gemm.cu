@@ -22,7 +22,7 @@
 // 28672: 295 - 303 us, 3.18 - 3.26 POPS, where the library's 8192^3 product
 // runs at 2.85; 2560 -> 6912: 27.4 us, 2.64 POPS); with up to 128 tokens and
 // large matrices the weights' stream (32 tokens, 8192 -> 28672: 43 us, 5.5
-// TB/s; 2560 -> 128000: 54 us, 6.2 TB/s), which is why the tile width is free:
+// TB/s; 2560 -> 128000: 55 us, 6.0 TB/s), which is why the tile width is free:
 // the tiles should come out even over the SMs (448 tiles of 64 or 224 of 128
 // channels for 148 SMs leave a quarter of the time idle, 138 of 208 none);
 // and in between the latency of a tile's k-blocks, which the split shortens.
