@@ -19,10 +19,11 @@
 // codes), 8 backward (z, dv, dz_in, dz; 10 with fp32 dv).  To get there the
 // arithmetic has to stay small: sums in bf16 pairs, packed fp32 products,
 // maxima as integers, codes by an addition, 1 / rms by Newton's method.
-// 8192 x 8192 bf16 forward took 126 us in scalar arithmetic and takes 78 (91%
-// of the copy rate); backward 167 us, and 93 - 95 (86 - 88%).  2048 x 2560
-// (one wave, 5.6 us of traffic) takes 10.9 us forward and 16.1 backward, of
-// which 5 are the closing kernel's boundary and its sum.
+// 8192 x 8192 bf16 forward took 126 us in scalar arithmetic, 78 - 80 in pairs
+// and takes 72 - 75 (96 - 99% of the copy rate, by where the tensors lie) with
+// the next tokens read ahead into L2; backward 167 us, 96 and 92 (89%).  2048
+// x 2560 (one wave, 5.6 us of traffic) takes 11 us forward and 15.7 backward,
+// of which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,6 +38,11 @@ namespace {
 
 __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Memory that another token will want, from HBM as far as L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(static_cast<uint32_t>(bytes)));
 }
 
 template <typename V, typename Op>
@@ -106,10 +112,15 @@ struct AddNormParams {
 // longer than that too, z is read back for the absmax and again for the
 // codes; either way each thread reads only what it wrote.  kFull: every thread
 // has all its chunks, so their instructions interleave without bounds between
-// them (2048 x 2560 fp32 16.7 -> 14.6 us).
-template <typename T, int C, bool kFull>
+// them (2048 x 2560 fp32 16.7 -> 14.6 us).  kAhead: x and residual of the
+// token `ahead` tokens on come as far as L2 while this one is worked on, so
+// that HBM does not stand still while the blocks of an SM, which began
+// together, all compute or store.  Not before this token's own loads are in:
+// asked for at the start they delay those (8192 x 2560 30.4 - 31.8 us, 29.5
+// after the first sum; 32.9 without).
+template <typename T, int C, bool kFull, bool kAhead>
 __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
-                                                                                         int staged) {
+                                                                                         int staged, int ahead) {
   extern __shared__ uint4 row_buf[];
   constexpr int N = kPer<T>;
   __shared__ double red_d[kMaxGroupWarps];
@@ -207,6 +218,11 @@ __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_qua
                                  red_d + group * W, W, wig, lane, bar);
   const float r = rstd_of(ss, P.K, P.inv_k, P.eps);
   r2 = pack2(r, r);
+  if (kAhead && tid == 0 && P.M - m > ahead) {
+    const size_t at = row + static_cast<size_t>(ahead) * P.K;
+    prefetch_l2(static_cast<const T*>(P.x) + at, P.K * sizeof(T));
+    prefetch_l2(static_cast<const T*>(P.res) + at, P.K * sizeof(T));
+  }
 
   uint32_t top = 0;
   if constexpr (C > 0) {
@@ -316,22 +332,43 @@ cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stre
   const dim3 grid((P.M + groups - 1) / groups);
   const int held = n <= 2 ? n : 4;
   const bool full = chunks == held * 32 * W;  // every thread holds as many chunks as it has room for
-  auto run = [&](auto with_bounds, auto without) {
-    return launch(full ? without : with_bounds, grid, dim3(threads), 0, stream, pdl, P, W, 0);
-  };
-  if (n <= 1) return run(add_rmsnorm_quant_kernel<T, 1, false>, add_rmsnorm_quant_kernel<T, 1, true>);
-  if (n <= 2) return run(add_rmsnorm_quant_kernel<T, 2, false>, add_rmsnorm_quant_kernel<T, 2, true>);
-  if (n <= 4) return run(add_rmsnorm_quant_kernel<T, 4, false>, add_rmsnorm_quant_kernel<T, 4, true>);
   const size_t row = static_cast<size_t>(P.K) * sizeof(T);
-  const bool staged = row <= kMaxRowBytes;
+  const bool staged = n > 4 && row <= kMaxRowBytes;
+  // Reading ahead pays where enough tokens wait behind those that what the
+  // registers and the staged rows let be resident, and over a distance of half
+  // to all of these (8192 x 8192 78.0 us without, 78.4, 73.2, 72.4 and 72.5 at
+  // 1/4, 1/2, 3/4 and all; 1021 fp32 tokens of 8640 26.0, and 24.2, 24.1, 24.5
+  // and 24.2; 700 x 4096, 1.2 waves: 7.3 without, 7.6 with; 512 x 28672, two
+  // resident per SM, 1.7 waves: 28.6 and 29.1).
+  int per_sm = (n <= 2 ? 1536 : 1024) / threads;
+  if (n > 4) per_sm = staged ? std::min(per_sm, static_cast<int>(228 * 1024 / (row + 2048))) : 0;
+  const long long resident = static_cast<long long>(num_sms()) * per_sm * groups;
+  const bool waits = per_sm > 0 && 2 * P.M > (per_sm > 2 ? 3 : 4) * resident;
+  const int ahead = static_cast<int>(n <= 4 ? resident / 4 * 3 : resident / 2);
+  auto run = [&](auto some, auto all, auto some_ahead, auto all_ahead) {
+    return launch(waits ? (full ? all_ahead : some_ahead) : (full ? all : some), grid, dim3(threads), 0, stream, pdl, P,
+                  W, 0, ahead);
+  };
+  if (n <= 1)
+    return run(add_rmsnorm_quant_kernel<T, 1, false, false>, add_rmsnorm_quant_kernel<T, 1, true, false>,
+               add_rmsnorm_quant_kernel<T, 1, false, true>, add_rmsnorm_quant_kernel<T, 1, true, true>);
+  if (n <= 2)
+    return run(add_rmsnorm_quant_kernel<T, 2, false, false>, add_rmsnorm_quant_kernel<T, 2, true, false>,
+               add_rmsnorm_quant_kernel<T, 2, false, true>, add_rmsnorm_quant_kernel<T, 2, true, true>);
+  if (n <= 4)
+    return run(add_rmsnorm_quant_kernel<T, 4, false, false>, add_rmsnorm_quant_kernel<T, 4, true, false>,
+               add_rmsnorm_quant_kernel<T, 4, false, true>, add_rmsnorm_quant_kernel<T, 4, true, true>);
+  auto* kernel = waits ? add_rmsnorm_quant_kernel<T, 0, false, true> : add_rmsnorm_quant_kernel<T, 0, false, false>;
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMaxRowBytes);
+    const cudaError_t e1 = cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false, false>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
+    return e1 != cudaSuccess ? e1
+                             : cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false, true>,
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch(add_rmsnorm_quant_kernel<T, 0, false>, grid, dim3(threads), staged ? row : 0, stream, pdl, P, W,
-                staged ? 1 : 0);
+  return launch(kernel, grid, dim3(threads), staged ? row : 0, stream, pdl, P, W, staged ? 1 : 0, ahead);
 }
 
 // ---------------------------------------------------------------------------
@@ -433,7 +470,10 @@ struct AddNormBackParams {
   int M, K;
   double inv_k;
   float inv_kf;
+  int ahead = 0;       // kAheadIn, kAheadRing
 };
+
+constexpr int kAheadIn = 1, kAheadRing = 2;
 
 // N gradient values of type TD: 8, 16 or 32 bytes.
 template <typename TD, int N>
@@ -661,6 +701,17 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
     return warp_sum2(pack2(a0 + a1, b0 + b1));
   };
 
+  // From HBM as far as L2: dz_in of the next token, z and dv of the one behind
+  // the ring's.
+  auto ahead_in = [&](size_t row) {
+    prefetch_l2(static_cast<const T*>(P.dz_in) + (row + static_cast<size_t>(stride) * P.K), P.K * sizeof(T));
+  };
+  auto ahead_ring = [&](size_t row) {
+    const size_t at = row + static_cast<size_t>(3 * stride) * P.K;
+    prefetch_l2(static_cast<const T*>(P.z) + at, P.K * sizeof(T));
+    prefetch_l2(static_cast<const TD*>(P.dv) + at, P.K * sizeof(TD));
+  };
+
   request(g0, 0);
   request(g0 + stride, 1);
   copy_async_wait<1>();
@@ -677,6 +728,17 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
   for (int m = g0; m < P.M; m += stride, parity ^= 1) {
     const size_t row = static_cast<size_t>(m) * P.K;
     const int s1 = s == R::kStages - 1 ? 0 : s + 1, s2 = s1 == R::kStages - 1 ? 0 : s1 + 1;
+    if constexpr (R::kStages == 3) {
+      if (P.ahead && tid == 0) {
+        if (P.dz_in && (P.ahead & kAheadIn) && m + stride < P.M) ahead_in(row);
+        if ((P.ahead & kAheadRing) && m + 3 * stride < P.M) ahead_ring(row);
+      }
+    } else if constexpr (C == 4 && !kCluster) {
+      if (wig == 0 && lane == 0) {
+        if (P.dz_in && m + stride < P.M) ahead_in(row);
+        if (m + 3 * stride < P.M) ahead_ring(row);
+      }
+    }
     uint4 in[C];
     if (P.dz_in) {
 #pragma unroll
@@ -948,11 +1010,11 @@ BackPlan plan_backward(int M, int K, int per, int piece) {
   // Chunks per thread: one while a warp holds the token, two while eight do, else four.
   p.C = chunks <= 32 ? 1 : chunks <= 512 ? 2 : 4;
   // Longer than eight warps of four chunks hold: a cluster of such blocks (512
-  // tokens of 28672: 35 us bf16, 57 fp32; read twice by one block each and a
+  // tokens of 28672: 34 us bf16, 50 fp32; read twice by one block each and a
   // third time for the gain 44 and 80; 1024 bf16 tokens of 8640 with fp32
   // gradients 29.5 us, 31.3 in one block of nine warps), unless 12 or 16 warps
   // hold it, an even share for an SM's four schedulers (4096 fp32 tokens of
-  // 8192: 88.5 us, 91.8 in clusters of two); or a cluster of up to sixteen
+  // 8192: 87 us, 91.8 in clusters of two); or a cluster of up to sixteen
   // warps where eight CTAs of eight are too few.
   p.cluster = 1;
   const int warps = (chunks - 1) / (32 * 4) + 1;
@@ -1030,6 +1092,16 @@ template <typename T, typename TD>
 cudaError_t launch_back_t(AddNormBackParams P, float* dgain, cudaStream_t stream) {
   const BackPlan p = plan_backward(P.M, P.K, kPer<T>, BackRing<T, TD>::kChunk);
   if (!dgain) P.part = nullptr;
+  // (8192 x 8192 bf16 96.1 -> 92.3 us, with dz_in alone 96.3 and with z and dv
+  // alone 97.3; 8192 x 2560 51.1 -> 46.4; 8192 x 1024, many short tokens, 19.3,
+  // and 20.0 with both.  fp32 tokens and clusters, which have twice and more of
+  // a token under way in the ring, do best with dz_in: 512 x 28672 bf16 35.5 ->
+  // 33.8, 34.8 with both; 4096 x 8192 fp32 89.7 -> 87.1 and 89.7.)
+  if (sizeof(T) == 4 || p.cluster > 1) {
+    P.ahead = kAheadIn;
+  } else if (P.K >= 2048) {
+    P.ahead = kAheadIn | kAheadRing;
+  }
   cudaError_t e;
   if (p.C == 0) {
     if (!dgain) P.rstd = nullptr;

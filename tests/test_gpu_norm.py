@@ -186,6 +186,35 @@ def test_backward_parity(M, K, dtype, grad, with_gain, past):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(20000, 192), (9000, 512), (5000, 1024), (3100, 2048), (3001, 2560), (2500, 8192), (1300, 8640),
+                                 (1300, 16384), (700, 28672), (700, 40960)])
+def test_many_tokens(M, K, dtype):
+    """Several waves of tokens: the codes of rmsnorm_quant, in place too, and gradients as in calls of few tokens."""
+    dt = DT[dtype]
+    gen = torch.Generator("cuda").manual_seed(M)
+    x, res, d = (torch.randn((M, K), device="cuda", generator=gen).to(dt) for _ in range(3))
+    g = dev(_gain(K, K))
+    z, q, s, r = tb.add_rmsnorm_quant(x, res, g)
+    assert torch.equal(z, (x.float() + res.float()).to(dt))
+    q2, s2, r2 = tb.rmsnorm_quant(z, g)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and torch.equal(r, r2)
+    dz, dgain = tb.add_rmsnorm_backward(z, d, g, dz_in=x)
+    for at in (0, M // 3, M - 70):
+        part, _ = tb.add_rmsnorm_backward(z[at:at + 70], d[at:at + 70], g, dz_in=x[at:at + 70])
+        assert torch.equal(part, dz[at:at + 70])
+    zd, dd = z.double(), d.double()
+    n = zd / ((zd * zd).mean(1, keepdim=True) + float(np.float32(1e-6))).sqrt()
+    bar = U * (23 + -(-M // 64) + 148 + 32) * (dd * n).abs().sum(0)
+    assert ((dgain - (dd * n).sum(0)).abs() <= bar).all()
+    kept = x.clone()
+    z3, q3, s3, _ = tb.add_rmsnorm_quant(x, res, g, z=x)
+    assert z3 is x and torch.equal(z3, z) and torch.equal(q3, q) and torch.equal(s3, s)
+    dz3, _ = tb.add_rmsnorm_backward(z, d, g, dz_in=kept, dz=kept)
+    assert dz3 is kept and torch.equal(kept, dz)
+
+
+@pytest.mark.gpu
 def test_backward_against_differences():
     """Directional derivatives of L = <d, norm(z)> + <dz_in, z> by central differences in 64 bits."""
     M, K, eps = 6, 640, 1e-5
