@@ -22,7 +22,7 @@
 // 8192 x 8192 bf16 forward took 126 us in scalar arithmetic, 78 - 80 in pairs
 // and takes 72 - 75 (96 - 99% of the copy rate, by where the tensors lie) with
 // the next tokens read ahead into L2; backward 167 us, 96 and 92 (89%).  2048
-// x 2560 (one wave, 5.6 us of traffic) takes 11 us forward and 15.7 backward,
+// x 2560 (one wave, 5.6 us of traffic) takes 11.6 us forward and 15.7 backward,
 // of which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
 
@@ -116,10 +116,11 @@ struct AddNormParams {
 // token `ahead` tokens on come as far as L2 while this one is worked on, so
 // that HBM does not stand still while the blocks of an SM, which began
 // together, all compute or store.  Not before this token's own loads are in:
-// asked for at the start they delay those (8192 x 2560 30.4 - 31.8 us, 29.5
-// after the first sum; 32.9 without).
-template <typename T, int C, bool kFull, bool kAhead>
-__global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
+// asked for at the start they delay those (8192 x 2560 in four chunks 30.4 -
+// 31.8 us, 29.5 after the first sum; 32.9 without).  kRoom: for blocks of at
+// most 256 threads, three of which share an SM's registers.
+template <typename T, int C, bool kFull, bool kAhead, bool kRoom>
+__global__ void __launch_bounds__(kRoom ? 256 : 512, C == 4 && !kRoom || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
                                                                                          int staged, int ahead) {
   extern __shared__ uint4 row_buf[];
   constexpr int N = kPer<T>;
@@ -324,51 +325,91 @@ Groups plan_groups(int M, int chunks) {
   return g;
 }
 
+using AddNormKernel = void (*)(AddNormParams, int, int, int);
+
+cudaError_t launch_add_rmsnorm_quant_k(AddNormKernel kernel, const AddNormParams& P, const Groups& g, int ahead, size_t smem,
+                                       cudaStream_t stream, bool pdl) {
+  return launch(kernel, dim3((P.M + g.groups - 1) / g.groups), dim3(32 * g.W * g.groups), smem, stream, pdl, P, g.W,
+                smem ? 1 : 0, ahead);
+}
+
+template <typename T, int C, bool kRoom>
+cudaError_t launch_add_rmsnorm_quant_c(const AddNormParams& P, const Groups& g, bool full, int ahead, size_t smem,
+                                       cudaStream_t stream, bool pdl) {
+  AddNormKernel kernel = ahead ? add_rmsnorm_quant_kernel<T, C, false, true, kRoom>
+                               : add_rmsnorm_quant_kernel<T, C, false, false, kRoom>;
+  if constexpr (C > 0) {
+    if (full)
+      kernel = ahead ? add_rmsnorm_quant_kernel<T, C, true, true, kRoom> : add_rmsnorm_quant_kernel<T, C, true, false, kRoom>;
+  } else {
+    static std::atomic<uint64_t> attr_done{0};
+    const cudaError_t e = once_per_device(attr_done, [] {
+      const AddNormKernel both[] = {add_rmsnorm_quant_kernel<T, C, false, true, kRoom>,
+                                    add_rmsnorm_quant_kernel<T, C, false, false, kRoom>};
+      for (AddNormKernel k : both) {
+        const cudaError_t e1 = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
+        if (e1 != cudaSuccess) return e1;
+      }
+      return cudaSuccess;
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_add_rmsnorm_quant_k(kernel, P, g, ahead, smem, stream, pdl);
+}
+
 template <typename T>
 cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stream, bool pdl) {
   const int chunks = P.K / kPer<T>;
-  const Groups g = plan_groups(P.M, chunks);
-  const int W = g.W, n = g.n, groups = g.groups, threads = 32 * W * groups;
-  const dim3 grid((P.M + groups - 1) / groups);
-  const int held = n <= 2 ? n : 4;
-  const bool full = chunks == held * 32 * W;  // every thread holds as many chunks as it has room for
+  Groups g = plan_groups(P.M, chunks);
+  int held = g.n <= 2 ? g.n : g.n <= 4 ? 4 : 0;
+  // 80 registers a thread and 24 warps per SM (kRoom) in place of 64 and 32.
+  // Four chunks of bf16 that every thread has: 2048 x 5120 16.6 us, 19.1 with
+  // 64; 2048 x 4096 14.0 and 15.9; 700 x 4096 6.6 and 7.3; but with whole
+  // schedulers per token and many waves the warps count more: 8192 x 8192 78.4
+  // and 74.9, 16384 x 4096 75.6 and 72.8, 8192 x 4096 40.7 and 40.9; nor where
+  // 32 warps make one wave and 24 do not: 4096 x 1024 8.7 and 7.6.  fp32 has
+  // its room in 64: 4096 x 2048 19.9 and 19.1.
+  const bool fills = held == 4 && chunks == 4 * 32 * g.W;
+  const long long sms = num_sms(), warps = static_cast<long long>(P.M) * g.W;
+  bool room = fills && sizeof(T) == 2 && g.W <= kNormThreads / 32 && (g.W % 4 != 0 || warps <= 240 * sms) &&
+              (warps <= 24 * sms || warps > 32 * sms);
+  // Five chunks where every thread has five and would lack some of four, or
+  // where they spare more than eight warps, and 24 warps per SM have work: 8192
+  // x 2560 27.3 us, 31.5 with four; 2048 x 10240 29.0 and 35.7; 4096 x 1280
+  // fp32 13.3 and 17.0; 1021 x 8640 18.5 and 19.4; 1024 x 2560 6.8 and 6.6.
+  const int five = (chunks + 159) / 160;
+  const bool spares = g.W > kNormThreads / 32 || (held == 4 && !fills && chunks == 160 * five);
+  if (spares && five <= kNormThreads / 32 && static_cast<long long>(P.M) * five >= 24 * sms) {
+    held = 5;
+    room = true;
+    g = Groups{5, five, kNormThreads / 32 / five};
+  }
+  const bool full = chunks == held * 32 * g.W;  // every thread holds as many chunks as it has room for
   const size_t row = static_cast<size_t>(P.K) * sizeof(T);
-  const bool staged = n > 4 && row <= kMaxRowBytes;
+  const size_t smem = held == 0 && row <= kMaxRowBytes ? row : 0;
   // Reading ahead pays where enough tokens wait behind those that what the
   // registers and the staged rows let be resident, and over a distance of half
   // to all of these (8192 x 8192 78.0 us without, 78.4, 73.2, 72.4 and 72.5 at
   // 1/4, 1/2, 3/4 and all; 1021 fp32 tokens of 8640 26.0, and 24.2, 24.1, 24.5
   // and 24.2; 700 x 4096, 1.2 waves: 7.3 without, 7.6 with; 512 x 28672, two
   // resident per SM, 1.7 waves: 28.6 and 29.1).
-  int per_sm = (n <= 2 ? 1536 : 1024) / threads;
-  if (n > 4) per_sm = staged ? std::min(per_sm, static_cast<int>(228 * 1024 / (row + 2048))) : 0;
-  const long long resident = static_cast<long long>(num_sms()) * per_sm * groups;
-  const bool waits = per_sm > 0 && 2 * P.M > (per_sm > 2 ? 3 : 4) * resident;
-  const int ahead = static_cast<int>(n <= 4 ? resident / 4 * 3 : resident / 2);
-  auto run = [&](auto some, auto all, auto some_ahead, auto all_ahead) {
-    return launch(waits ? (full ? all_ahead : some_ahead) : (full ? all : some), grid, dim3(threads), 0, stream, pdl, P,
-                  W, 0, ahead);
-  };
-  if (n <= 1)
-    return run(add_rmsnorm_quant_kernel<T, 1, false, false>, add_rmsnorm_quant_kernel<T, 1, true, false>,
-               add_rmsnorm_quant_kernel<T, 1, false, true>, add_rmsnorm_quant_kernel<T, 1, true, true>);
-  if (n <= 2)
-    return run(add_rmsnorm_quant_kernel<T, 2, false, false>, add_rmsnorm_quant_kernel<T, 2, true, false>,
-               add_rmsnorm_quant_kernel<T, 2, false, true>, add_rmsnorm_quant_kernel<T, 2, true, true>);
-  if (n <= 4)
-    return run(add_rmsnorm_quant_kernel<T, 4, false, false>, add_rmsnorm_quant_kernel<T, 4, true, false>,
-               add_rmsnorm_quant_kernel<T, 4, false, true>, add_rmsnorm_quant_kernel<T, 4, true, true>);
-  auto* kernel = waits ? add_rmsnorm_quant_kernel<T, 0, false, true> : add_rmsnorm_quant_kernel<T, 0, false, false>;
-  static std::atomic<uint64_t> attr_done{0};
-  const cudaError_t e = once_per_device(attr_done, [] {
-    const cudaError_t e1 = cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false, false>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
-    return e1 != cudaSuccess ? e1
-                             : cudaFuncSetAttribute(add_rmsnorm_quant_kernel<T, 0, false, true>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowBytes);
-  });
-  if (e != cudaSuccess) return e;
-  return launch(kernel, grid, dim3(threads), staged ? row : 0, stream, pdl, P, W, staged ? 1 : 0, ahead);
+  int per_sm = (room ? 768 : held == 1 || held == 2 ? 1536 : 1024) / (32 * g.W * g.groups);
+  if (held == 0) per_sm = smem ? std::min(per_sm, static_cast<int>(228 * 1024 / (row + 2048))) : 0;
+  const long long resident = sms * per_sm * g.groups;
+  int ahead = 0;
+  if (per_sm > 0 && 2LL * P.M > (per_sm > 2 ? 3 : 4) * resident)
+    ahead = static_cast<int>(held ? resident / 4 * 3 : resident / 2);
+  if (held == 1) return launch_add_rmsnorm_quant_c<T, 1, false>(P, g, full, ahead, 0, stream, pdl);
+  if (held == 2) return launch_add_rmsnorm_quant_c<T, 2, false>(P, g, full, ahead, 0, stream, pdl);
+  if (held == 5) return launch_add_rmsnorm_quant_c<T, 5, true>(P, g, full, ahead, 0, stream, pdl);
+  if constexpr (sizeof(T) == 2) {
+    if (room)
+      return launch_add_rmsnorm_quant_k(ahead ? add_rmsnorm_quant_kernel<T, 4, true, true, true>
+                                              : add_rmsnorm_quant_kernel<T, 4, true, false, true>,
+                                        P, g, ahead, 0, stream, pdl);
+  }
+  if (held == 4) return launch_add_rmsnorm_quant_c<T, 4, false>(P, g, full, ahead, 0, stream, pdl);
+  return launch_add_rmsnorm_quant_c<T, 0, false>(P, g, false, ahead, smem, stream, pdl);
 }
 
 // ---------------------------------------------------------------------------
