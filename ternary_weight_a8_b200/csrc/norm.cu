@@ -120,8 +120,8 @@ struct AddNormParams {
 // 31.8 us, 29.5 after the first sum; 32.9 without).  kRoom: for blocks of at
 // most 256 threads, three of which share an SM's registers.
 template <typename T, int C, bool kFull, bool kAhead, bool kRoom>
-__global__ void __launch_bounds__(kRoom ? 256 : 512, C == 4 && !kRoom || C == 0 ? 2 : 3) add_rmsnorm_quant_kernel(const AddNormParams P, int W,
-                                                                                         int staged, int ahead) {
+__global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 0 ? 2 : 3)
+    add_rmsnorm_quant_kernel(const AddNormParams P, int W, int staged, int ahead) {
   extern __shared__ uint4 row_buf[];
   constexpr int N = kPer<T>;
   __shared__ double red_d[kMaxGroupWarps];
