@@ -393,9 +393,14 @@ __device__ __forceinline__ float round_to(float v) {
 // ---------------------------------------------------------------------------
 // Misc
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint4 ldg_stream_u4(const void* p) {
+// Memory that is read once.  A coherent load, since a kernel launched as a
+// programmatic dependent is already resident while the kernel before it
+// writes: the read-only path (.nc, __ldg) is only for memory that nothing
+// writes during the kernel's life, and the compiler may lift such a load over
+// griddep_wait.
+__device__ __forceinline__ uint4 ld_stream_u4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;

@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) i8_gemm_kernel(const __grid_constant
           const bool ch = i < bn;
           const int at = ch ? (first / T.m_tiles) * bn + i : (first % T.m_tiles) * kBM + i - bn;
           rec[ch ? i : kMaxBN + i - bn] =
-              at < (ch ? P.N : P.M) ? __frcp_rn(__ldg((ch ? P.wscale : P.scale) + at)) : 0.0f;
+              at < (ch ? P.N : P.M) ? __frcp_rn(__ldcg((ch ? P.wscale : P.scale) + at)) : 0.0f;
         }
       }
       // The int32 sums of this CTA's k-blocks, token rows of BN, over the ring
@@ -387,13 +387,13 @@ __global__ void __launch_bounds__(kThreads) i8_gemm_kernel(const __grid_constant
         float* rwt = rw + a * kMaxBN;
         for (int i = threadIdx.x - 128; i < bn; i += 128) {
           const int n = nt * bn + i;
-          rwt[i] = n < P.N ? __frcp_rn(__ldg(P.wscale + n)) : 0.0f;
+          rwt[i] = n < P.N ? __frcp_rn(__ldcg(P.wscale + n)) : 0.0f;
         }
         // One of the four gave up: all leave together (a warp that left alone would strand the rest here).
         if (epi_any(failed)) break;
         const int m0 = mt * kBM * CG + static_cast<int>(rank) * kBM + q * 32;  // first token of this warp
         const int m = m0 + lane;
-        const float rs = m < P.M ? __frcp_rn(__ldg(P.scale + m)) : 0.0f;
+        const float rs = m < P.M ? __frcp_rn(__ldcg(P.scale + m)) : 0.0f;
         // tcgen05.ld below is warp-collective: take the wait's outcome warp-wide.
         const bool got = wait_bar<CG>(tfull_bar(a), (tc >> 1) & 1, ctl, peer_abort);
         const bool go = __all_sync(0xffffffffu, got);

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(32 * kGvWarps, BPS)
 #pragma unroll
       for (int i = 0; i < 2 * MT; ++i) {
         if (!decltype(cut)::value || c + u < c1) {
-          a[u][i] = ldg_stream_u4(wp[i] + 64 * (c + u));
+          a[u][i] = ld_stream_u4(wp[i] + 64 * (c + u));
         } else {
           a[u][i] = make_uint4(0, 0, 0, 0);
         }
@@ -212,6 +212,18 @@ __global__ void __launch_bounds__(32 * kGvWarps, BPS)
     use(c, a, cut);
   }
 
+  // The scales of this thread's outputs, under way while the sums meet (read
+  // where they are used: 32 tokens, 4096 -> 6912 10.1 us, 9.1 here; 1 token,
+  // 2560 -> 128000 52.2 and 50.3; before the loop their registers are missed
+  // there: 10.5 and 51.3).
+  constexpr int kOuts = (8 * TG * kRows + 32 * kGvWarps - 1) / (32 * kGvWarps);
+  float sx[kOuts], sw[kOuts];
+#pragma unroll
+  for (int o = 0; o < kOuts; ++o) {
+    const int i = threadIdx.x + o * 32 * kGvWarps, m = i / kRows, n = n0 + i % kRows;
+    sx[o] = !kRaw && m < P.M ? __ldcg(P.scale + m) : 1.0f;
+    sw[o] = n < P.N ? __ldcg(P.wscale + n) : 1.0f;
+  }
   __syncthreads();  // the sums are zero
   // Fragment (row g or g + 8, tokens 2t and 2t + 1) of every group; integer
   // sums, so the warps' order does not matter.
@@ -224,11 +236,12 @@ __global__ void __launch_bounds__(32 * kGvWarps, BPS)
         red_shared_add(&sums[8 * j + 2 * t + (i & 1)][16 * r + g + 8 * (i >> 1)], acc[r][j][i]);
   __syncthreads();
   TY* y = static_cast<TY*>(P.y);
-  for (int i = threadIdx.x; i < 8 * TG * kRows; i += 32 * kGvWarps) {
-    const int m = i / kRows, r = i % kRows, n = n0 + r;
-    if (m >= P.M || n >= P.N) continue;
+#pragma unroll
+  for (int o = 0; o < kOuts; ++o) {
+    const int i = threadIdx.x + o * 32 * kGvWarps, m = i / kRows, r = i % kRows, n = n0 + r;
+    if (i >= 8 * TG * kRows || m >= P.M || n >= P.N) continue;
     const int sum = sums[m][r];
-    const float f = __fmul_rn(__frcp_rn(kRaw ? raw_scales[m] : __ldg(P.scale + m)), __frcp_rn(__ldg(P.wscale + n)));
+    const float f = __fmul_rn(__frcp_rn(kRaw ? raw_scales[m] : sx[o]), __frcp_rn(sw[o]));
     const size_t at = static_cast<size_t>(m) * P.N + n;
     const float v = __fmul_rn(static_cast<float>(sum), f);
     if constexpr (sizeof(TY) == 2) {
