@@ -28,16 +28,19 @@ namespace bl {
 constexpr int kTile = 64;
 
 // tt[k][n] = t[n][k] as bf16, from packed [N][K/4] (element 16g+4j+b in byte b, bits 2j..2j+1 of word g).
-__global__ void __launch_bounds__(256) unpack_transpose_kernel(const uint32_t* __restrict__ packed, int N, int K,
-                                                               __nv_bfloat16* __restrict__ tt) {
+// The wait is also what the GEMM behind this kernel relies on: its own wait is
+// for this kernel alone, so dy is complete only if this one has waited for it.
+__global__ void __launch_bounds__(256) unpack_transpose_kernel(const uint32_t* packed, int N, int K, __nv_bfloat16* tt) {
   __shared__ __nv_bfloat16 tile[kTile][kTile + 2];  // [k][n], padded
+  griddep_launch_dependents();
+  griddep_wait();  // tt may still be read by the preceding kernel
   const int n0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
   const int words = K / 16;
   // 64 rows x 4 words (64 inputs) of the packed tile: one word per thread.
   const int r = threadIdx.x >> 2, wi = threadIdx.x & 3;
   const int n = n0 + r;
   uint32_t w = 0x55555555u;  // code 1 (t = 0) outside the matrix
-  if (n < N) w = __ldg(packed + static_cast<size_t>(n) * words + k0 / 16 + wi);
+  if (n < N) w = __ldcg(packed + static_cast<size_t>(n) * words + k0 / 16 + wi);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -61,9 +64,10 @@ __global__ void __launch_bounds__(256) unpack_transpose_kernel(const uint32_t* _
 
 // out[c][r] = f(in[r][c]) for a [R][C] bf16 matrix, or (xhat) bf16(q[r][c] / s[r]) from int8 codes.
 template <bool kFromCodes>
-__global__ void __launch_bounds__(256) transpose_kernel(const void* __restrict__ in, const float* __restrict__ s,
-                                                        int R, int C, __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(256) transpose_kernel(const void* in, const float* s, int R, int C, __nv_bfloat16* out) {
   __shared__ __nv_bfloat16 tile[kTile][kTile + 2];  // [r][c], padded
+  griddep_launch_dependents();
+  griddep_wait();  // the input may be the preceding kernel's output; out may still be read by it
   const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
   for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
     const int rr = i / kTile, cc = i % kTile;
@@ -72,7 +76,7 @@ __global__ void __launch_bounds__(256) transpose_kernel(const void* __restrict__
     if (r < R && c < C) {
       if constexpr (kFromCodes) {
         const int8_t q = static_cast<const int8_t*>(in)[static_cast<size_t>(r) * C + c];
-        v = __float2bfloat16_rn(__fdiv_rn(static_cast<float>(q), __ldg(s + r)));
+        v = __float2bfloat16_rn(__fdiv_rn(static_cast<float>(q), __ldcg(s + r)));
       } else {
         v = static_cast<const __nv_bfloat16*>(in)[static_cast<size_t>(r) * C + c];
       }
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kFThreads, 1) gemm_bf16_kernel(const __grid_co
     }
   } else if (warp >= 4) {
     const int q = warp & 3;
-    const float al = alpha_ptr ? __fmul_rn(alpha, __ldg(alpha_ptr)) : alpha;
+    const float al = alpha_ptr ? __fmul_rn(alpha, __ldcg(alpha_ptr)) : alpha;
     int tc = 0;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++tc) {
       const int pt = tile % p_tiles, qt = tile / p_tiles;

@@ -23,7 +23,7 @@ def _code(name):
         return re.sub(r"//[^\n]*", "", fh.read())
 
 
-@pytest.mark.parametrize("name", ["common.cuh", "i8_gemv.cu", "i8_gemm.cu"])
+@pytest.mark.parametrize("name", ["common.cuh", "i8_gemv.cu", "i8_gemm.cu", "ste.cu"])
 def test_arguments_are_not_read_through_the_read_only_path(name):
     found = [m.group(0) for m in READ_ONLY.finditer(_code(name))]
     assert not found, "%s: %s" % (name, found)
@@ -32,3 +32,31 @@ def test_arguments_are_not_read_through_the_read_only_path(name):
 def test_the_pattern_sees_both_spellings():
     assert READ_ONLY.search("x = __ldg(p);") and READ_ONLY.search('asm("ld.global.nc.v4.u32 ...");')
     assert not READ_ONLY.search("__ldcg(p)") and not READ_ONLY.search('"ld.global.L1::no_allocate.v4.u32"')
+
+
+def _kernels(code):
+    """(name, body) of the file's __global__ functions that are not launched with <<<>>>."""
+    launch_bounds = r"(?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?(?:__maxnreg__\((?:[^()]|\([^()]*\))*\)\s*)?"
+    for m in re.finditer(r"__global__\s+void\s+" + launch_bounds + r"(\w+)\s*\(", code):
+        start = code.index("{", m.end())
+        depth, end = 0, start
+        while True:
+            depth += {"{": 1, "}": -1}.get(code[end], 0)
+            if depth == 0:
+                break
+            end += 1
+        if not re.search(m.group(1) + r"\s*<<<", code):
+            yield m.group(1), code[start:end]
+
+
+def test_every_dependent_kernel_waits_for_the_kernel_before_it():
+    """One that does not may read what is still being written, and lets the kernel behind it start as early: a wait is for
+    the preceding kernel only, which has to have waited itself."""
+    seen = set()
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".cu"):
+            for kernel, body in _kernels(_code(name)):
+                seen.add(kernel)
+                assert "griddep_wait()" in body, "%s: %s" % (name, kernel)
+    assert {"unpack_transpose_kernel", "transpose_kernel", "gemm_bf16_kernel", "i8_gemm_kernel", "gemv_group_kernel",
+            "gemm_kernel", "add_rmsnorm_backward_kernel", "act_quant_kernel"} <= seen
