@@ -159,21 +159,39 @@ __global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 
     }
   };
   f32x2 r2 = 0;
-  auto norm_chunk = [&](const uint4& zc, int c) {
+  // z r g of a chunk, its gains read here or already (`g`).
+  auto norm_chunk = [&](const uint4& zc, int c, const f32x2 (*g)[kPairs<T>] = nullptr) {
     f32x2 p[kPairs<T>];
     to_pairs<T>(zc, p);
 #pragma unroll
     for (int e = 0; e < kPairs<T>; ++e) p[e] = mul2(p[e], r2);
     if (P.gain) {
-      f32x2 g[kPairs<T>];
-      load_pairs(P.gain + static_cast<size_t>(c) * N, g);
+      f32x2 own[kPairs<T>];
+      if (!g) load_pairs(P.gain + static_cast<size_t>(c) * N, own);
 #pragma unroll
-      for (int e = 0; e < kPairs<T>; ++e) p[e] = mul2(p[e], g[e]);
+      for (int e = 0; e < kPairs<T>; ++e) p[e] = mul2(p[e], g ? (*g)[e] : own[e]);
     }
     return from_pairs<T>(p);
   };
 
   constexpr int CR = C > 0 ? C : 1;
+  // The gains of the first kGainFirst chunks are asked for with the token's
+  // own loads, those up to kGainNext behind the first sum, and the rest where
+  // they are used: as many early as the registers take without spilling (all
+  // where they are used: 4096 x 1280 fp32 16.1 us, 13.3 with all first; 2048 x
+  // 5120 bf16, four chunks with room, 18.1, 16.0 with 2 and 4, 17.2 with all
+  // first; 2048 x 2560 bf16, five chunks, 12.5, 11.2 with 3, 12.4 with 2 and 4;
+  // 64 x 8192 bf16, two chunks of 40 registers, 5.1 with none and 5.7 with any).
+  constexpr int kGainFirst = sizeof(T) == 4 || C <= 1 ? C : C == 2 ? 0 : C == 4 ? (kRoom ? 2 : kFull ? 0 : 1) : 3;
+  constexpr int kGainNext = kRoom && C == 4 ? 4 : kGainFirst;
+  f32x2 gains[kGainNext > 0 ? kGainNext : 1][kPairs<T>];
+  auto load_gains = [&](int first, int end) {
+    if (!P.gain) return;
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i >= first && i < end && (kFull || tid + i * step < chunks))
+        load_pairs(P.gain + static_cast<size_t>(tid + i * step) * N, gains[i < kGainNext ? i : 0]);
+  };
   uint4 keep[CR];
   if constexpr (C > 0) {
     uint4 other[CR];
@@ -185,6 +203,7 @@ __global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 
         other[i] = __ldcg(rr + c);
       }
     }
+    load_gains(0, kGainFirst);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
@@ -217,6 +236,7 @@ __global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 
   }
   const double ss = group_reduce(__dadd_rn(ss0, ss1), [](double a, double b) { return __dadd_rn(a, b); },
                                  red_d + group * W, W, wig, lane, bar);
+  load_gains(kGainFirst, kGainNext);
   const float r = rstd_of(ss, P.K, P.inv_k, P.eps);
   r2 = pack2(r, r);
   if (kAhead && tid == 0 && P.M - m > ahead) {
@@ -231,7 +251,7 @@ __global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 
     for (int i = 0; i < C; ++i) {
       const int c = tid + i * step;
       if (kFull || c < chunks) {
-        keep[i] = norm_chunk(keep[i], c);
+        keep[i] = norm_chunk(keep[i], c, i < kGainNext ? &gains[i < kGainNext ? i : 0] : nullptr);
         top = absmax16<T>(top, keep[i]);
         if (nr) nr[c] = keep[i];
       }

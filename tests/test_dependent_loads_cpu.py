@@ -23,7 +23,7 @@ def _code(name):
         return re.sub(r"//[^\n]*", "", fh.read())
 
 
-@pytest.mark.parametrize("name", ["common.cuh", "i8_gemv.cu", "i8_gemm.cu", "ste.cu"])
+@pytest.mark.parametrize("name", ["common.cuh", "pairs.cuh", "i8_gemv.cu", "i8_gemm.cu", "norm.cu", "ste.cu"])
 def test_arguments_are_not_read_through_the_read_only_path(name):
     found = [m.group(0) for m in READ_ONLY.finditer(_code(name))]
     assert not found, "%s: %s" % (name, found)

@@ -49,3 +49,25 @@ def _ternary(packed, K):
     words = packed.reshape(packed.shape[0], K // 16, 4)  # [N][g][b]
     t = np.stack([(words >> (2 * j)) & 3 for j in range(4)], axis=2)  # [N][g][j][b]
     return t.reshape(packed.shape[0], K).astype(np.int8) - 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 2560), (64, 8192), (513, 2560), (300, 4096), (40, 16384 + 64), (3, 131072 + 64)])
+def test_gains_written_just_before(M, K, dtype):
+    """Gains that the kernel just before the call wrote, as an optimiser's step does: every call reads the new ones."""
+    x = torch.randn((M, K), generator=torch.Generator("cuda").manual_seed(K), device="cuda").to(dtype)
+    sets = [torch.full((K,), 4.0 ** k, device="cuda") for k in range(3)]
+    want = []
+    for g in sets:
+        fwd = tb.add_rmsnorm_quant(x, x, g, x_norm=True)
+        torch.cuda.synchronize()
+        want.append((fwd, tb.add_rmsnorm_backward(x, x, g)))
+        torch.cuda.synchronize()
+    g = torch.empty_like(sets[0])
+    got = []
+    for k in range(30):
+        torch.mul(sets[k % 3], 1.0, out=g)
+        got.append((tb.add_rmsnorm_quant(x, x, g, x_norm=True), tb.add_rmsnorm_backward(x, x, g)))
+    for k, pair in enumerate(got):
+        for a, b in zip(pair[0] + pair[1], want[k % 3][0] + want[k % 3][1]):
+            assert torch.equal(a, b), k
