@@ -202,11 +202,15 @@ struct NormParams {
   int K;
 };
 
-// The gains of chunk c (16 floats).
+// The gains of chunk c (16 floats), which the kernel before may have written:
+// coherent loads, volatile so that none moves over a wait.
 __device__ __forceinline__ void load_gain16(const float* gain, int c, float4 (&g)[4]) {
   const float4* gp = reinterpret_cast<const float4*>(gain + 16 * c);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = __ldg(gp + i);
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(g[i].x), "=f"(g[i].y), "=f"(g[i].z), "=f"(g[i].w)
+                 : "l"(gp + i));
 }
 
 // v = round_to_TX(x * r [* g]) for the 16 inputs of a chunk, g its gains.

@@ -488,8 +488,8 @@ __global__ void __maxnreg__(128) gemm_kernel(
   } else if (warp >= C::kEpiWarp0) {
     const int q = warp & 3;  // tensor-memory lane quarter this warp may read
     griddep_wait();          // scales and row sums come from the preceding kernel; y may be read by it
-    const float gamma = __ldg(gamma_ptr);
-    const float gamma2 = is_glu ? __ldg(glu.gamma2) : 0.0f;
+    const float gamma = __ldcg(gamma_ptr);
+    const float gamma2 = is_glu ? __ldcg(glu.gamma2) : 0.0f;
     const bool staged = C::kOutWarpBytes > 0 && tma_out;
     uint8_t* obuf = smem + C::kOffOut + (warp - C::kEpiWarp0) * C::kOutWarpBytes;
     int ob = 0;  // staging buffer of the next box
@@ -511,9 +511,9 @@ __global__ void __maxnreg__(128) gemm_kernel(
       float gs = 0.0f, gs2 = 0.0f;
       int rs = 0;
       if (mvalid) {
-        gs = __fdiv_rn(gamma, __ldg(scale + m));
-        if (is_glu) gs2 = __fdiv_rn(gamma2, __ldg(scale + m));
-        rs = __ldg(rowsum + m);
+        gs = __fdiv_rn(gamma, __ldcg(scale + m));
+        if (is_glu) gs2 = __fdiv_rn(gamma2, __ldcg(scale + m));
+        rs = __ldcg(rowsum + m);
       }
       if (is_glu) {
         // 32 output columns at a time: the gate accumulators at column c, the

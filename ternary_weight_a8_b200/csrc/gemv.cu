@@ -821,8 +821,8 @@ __global__ void __launch_bounds__(kGvThreads, kGvBlocksPerSM) gemv_group_kernel(
       }
 
       // The epilogue's scalars, loaded now so their latency hides behind the products.
-      const float gamma = __ldg(L.gamma);
-      const float gamma_up = kGlu ? __ldg(P.layer[P.glu.up].gamma) : 0.0f;
+      const float gamma = __ldcg(L.gamma);
+      const float gamma_up = kGlu ? __ldcg(P.layer[P.glu.up].gamma) : 0.0f;
       int rsum_m[TG][2];
       float s_m[TG][2];
 #pragma unroll

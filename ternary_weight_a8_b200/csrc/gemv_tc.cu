@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) gemv_tc_kernel(const __grid_con
       const TcLayer& L = P.layer[layer_of(unit)];
       const int n = (unit - L.unit0) * kTcRows + r;
       if (n < L.N) {
-        const float gamma = __ldg(L.gamma);
+        const float gamma = __ldcg(L.gamma);
         TY* y = static_cast<TY*>(L.y);
 #pragma unroll
         for (int m = 0; m < kTcTok; ++m) {

@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t even_bits4(uint32_t x) {
 
 template <typename TY>
 __global__ void __launch_bounds__(kLutThreads) lut_gemv_kernel(const uint32_t* __restrict__ packed, const float* gamma_p,
-                                                               int N, int K, const int8_t* __restrict__ xq,
+                                                               int N, int K, const int8_t* xq,
                                                                const float* scale, const int32_t* rowsum,
                                                                TY* __restrict__ y, int32_t* __restrict__ acc_out) {
   extern __shared__ int16_t tab[];
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kLutThreads) lut_gemv_kernel(const uint32_t* _
   __syncthreads();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float gamma = __ldg(gamma_p);
+  const float gamma = __ldcg(gamma_p);
   const float gs = __fdiv_rn(gamma, __ldcg(scale));
   const int rs = __ldcg(rowsum);
   for (int n = blockIdx.x * kLutWarps + warp; n < N; n += gridDim.x * kLutWarps) {
