@@ -164,7 +164,9 @@ size_t bitlinear_add_rmsnorm_backward_workspace_bytes(int M, int K, int z_dtype)
  * gd = dnorm * gain:
  *   dz    = r * (gd - n * mean_k(gd * n)) + dz_in
  *   dgain = sum over tokens of dnorm * n
- * in fp32; dz is rounded once.
+ * in fp32; dz is rounded once.  The sums of z^2 and gd * z are taken in double
+ * where fp32 does not hold them (tokens around 1e25 or 1e-22, gradients beside
+ * them that overflow, or whose products fall below 2^-126).
  *   z       device [M][K] of z_dtype: the forward's z.
  *   dnorm   device [M][K] of dnorm_dtype (BL_F32 or BL_BF16): the gradient of
  *           the normalised activations.

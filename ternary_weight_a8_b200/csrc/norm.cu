@@ -25,6 +25,7 @@
 // x 2560 (one wave, 5.6 us of traffic) takes 11.6 us forward and 15.7 backward,
 // of which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include <algorithm>
 
@@ -604,9 +605,28 @@ __device__ __forceinline__ void store_pairs(float* p, const f32x2 (&v)[P2]) {
   }
 }
 
-// Sums of z^2 outside this range are taken again in double (fp32 squares
-// overflow above 2^128 and lose bits below 2^-126).
-constexpr float kSquaresLow = 1e-25f, kSquaresHigh = 1e37f;
+// Both sums of a token are taken again in double where fp32 may not hold them:
+//  - the sum of z^2 outside this range (fp32 squares overflow above 2^128 and
+//    lose bits below 2^-126);
+//  - the sum of gd * z no number, or overflowing with r;
+//  - that sum so small that the half steps of subnormal terms, 2^-150 each,
+//    may count: 2^26 of them are 2^-24 of 1e-30.  Zero is the sum of tokens
+//    without a gradient (padding, 8192 x 8192 91 us; taken again, 129), and
+//    up to r = 2^10 what it may hide is below 2^-140 of gradient.
+constexpr float kSquaresLow = 1e-25f, kSquaresHigh = 1e37f, kDotLow = 1e-30f, kDotZeroRstd = 1024.0f;
+
+__device__ __forceinline__ bool dot_in_range(float dot, float r) {
+  return fabsf(dot * r) < INFINITY && (fabsf(dot) > kDotLow || (dot == 0.0f && r <= kDotZeroRstd));
+}
+
+// gd * z of a pair in double, added to t.
+__device__ __forceinline__ double add_products(f32x2 gd, f32x2 z, double t) {
+  float g0, g1, z0, z1;
+  split2(gd, g0, g1);
+  split2(z, z0, z1);
+  t = __fma_rn(static_cast<double>(g0), static_cast<double>(z0), t);
+  return __fma_rn(static_cast<double>(g1), static_cast<double>(z1), t);
+}
 
 constexpr int kMaxCluster = 8;
 
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
   extern __shared__ uint4 ring[];
   constexpr int kSlots = kCluster ? kMaxGroupWarps * kMaxCluster : kMaxGroupWarps;
   __shared__ f32x2 red[2][kSlots];
-  __shared__ double red_d[kSlots];
+  __shared__ double red_d[2][kSlots];
   griddep_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -826,19 +846,26 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
     split2(both, ss, dot);
     both = next;
     float r = rsqrtf(fmaf(ss, P.inv_kf, P.eps));
-    if (!(ss > kSquaresLow && ss < kSquaresHigh)) {  // the same in the whole group
-      double t = 0.0;
+    float mean = dot * r * P.inv_kf;
+    const bool squares = !(ss > kSquaresLow && ss < kSquaresHigh);
+    if (squares || !dot_in_range(dot, r)) {  // the same in the whole group
+      double t = 0.0, u = 0.0;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         if (kFull || tid + i * step < chunks) {
-          f32x2 z[NP];
+          f32x2 z[NP], d[NP];
           z_of(s, i, z);
+          d_of(s, i, d);
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             float lo, hi;
             split2(z[e], lo, hi);
-            t = __fma_rn(static_cast<double>(lo), static_cast<double>(lo), t);
-            t = __fma_rn(static_cast<double>(hi), static_cast<double>(hi), t);
+            if (squares) {
+              t = __fma_rn(static_cast<double>(lo), static_cast<double>(lo), t);
+              t = __fma_rn(static_cast<double>(hi), static_cast<double>(hi), t);
+            }
+            if constexpr (kGain) d[e] = mul2(d[e], gains[i][e]);
+            u = add_products(d[e], z[e], u);
           }
         }
       }
@@ -846,22 +873,31 @@ __global__ void __launch_bounds__(C <= 2 ? 256 : 512, C == 1 ? 4 : C == 2 ? 3 : 
       if constexpr (kCluster) {
         cluster_sync_all();  // red_d may still be read for an earlier token
         t = warp_reduce(t, add);
-        if (lane < cl)
-          st_cluster_b64(mapa_shared(smem_u32(&red_d[rank * W + wig]), static_cast<uint32_t>(lane)),
+        u = warp_reduce(u, add);
+        if (lane < cl) {
+          st_cluster_b64(mapa_shared(smem_u32(&red_d[0][rank * W + wig]), static_cast<uint32_t>(lane)),
                          static_cast<f32x2>(__double_as_longlong(t)));
+          st_cluster_b64(mapa_shared(smem_u32(&red_d[1][rank * W + wig]), static_cast<uint32_t>(lane)),
+                         static_cast<f32x2>(__double_as_longlong(u)));
+        }
         cluster_sync_all();
-        t = red_d[0];
-        for (int i = 1; i < cl * W; ++i) t = add(t, red_d[i]);
+        t = red_d[0][0];
+        u = red_d[1][0];
+        for (int i = 1; i < cl * W; ++i) {
+          t = add(t, red_d[0][i]);
+          u = add(u, red_d[1][i]);
+        }
       } else {
         if (W > 1) group_sync(bar, 32 * W);  // red_d may still be read for an earlier token
-        t = group_reduce(t, add, red_d + group * W, W, wig, lane, bar);
+        t = group_reduce(t, add, red_d[0] + group * W, W, wig, lane, bar);
+        u = group_reduce(u, add, red_d[1] + group * W, W, wig, lane, bar);
       }
-      r = rstd_of(t, P.K, P.inv_k, P.eps);
+      if (squares) r = rstd_of(t, P.K, P.inv_k, P.eps);
+      mean = __double2float_rn(u * static_cast<double>(r) * P.inv_k);
     }
     // This token's sums are read and the next one's posted: the barrier may
     // begin, and is waited for once the token is written.
     if constexpr (kCluster) cluster_arrive_release();
-    const float mean = dot * r * P.inv_kf;
     const f32x2 r2 = pack2(r, r), mean2 = pack2(-mean, -mean);
     uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(P.dz) + row);
 #pragma unroll
@@ -973,7 +1009,18 @@ __global__ void __launch_bounds__(512, 2) add_rmsnorm_backward_long_kernel(const
   ss = group_reduce(ss, [](double a, double b) { return __dadd_rn(a, b); }, red_d, W, warp, lane, 1);
   dot = group_reduce(dot, [](float a, float b) { return a + b; }, red_f, W, warp, lane, 1);
   const float r = rstd_of(ss, P.K, P.inv_k, P.eps);
-  const float mean = dot * r * P.inv_kf;
+  float mean = dot * r * P.inv_kf;
+  if (!dot_in_range(dot, r)) {  // the same in the whole block
+    double u = 0.0;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+      f32x2 z[NP], gd[NP];
+      chunk(c, z, gd);
+#pragma unroll
+      for (int e = 0; e < NP; ++e) u = add_products(gd[e], z[e], u);
+    }
+    u = group_reduce(u, [](double a, double b) { return __dadd_rn(a, b); }, red_d, W, warp, lane, 1);
+    mean = __double2float_rn(u * static_cast<double>(r) * P.inv_k);
+  }
   const f32x2 r2 = pack2(r, r), mean2 = pack2(-mean, -mean);
   if (P.rstd && threadIdx.x == 0) P.rstd[m] = r;
 #pragma unroll 2
@@ -1055,7 +1102,7 @@ __global__ void __launch_bounds__(1024) gain_grad_finish_kernel(const float* __r
   }
 }
 
-constexpr int kRingMax = 224 * 1024;  // of a block's shared memory
+constexpr int kRingMax = 216 * 1024;  // of a block's shared memory, beside the static arrays
 
 // How the backward splits its work: from the sizes and the SM count alone, so
 // the workspace figure and the launch agree.
