@@ -39,12 +39,13 @@
  *    device memory.
  *  - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  *    only enqueue work; they do not synchronise, except
- *    bitlinear_device_status.
+ *    bitlinear_device_status and the other *_status calls.
  *  - Shapes: 1 <= N <= 2^24, 64 <= K, K % 64 == 0, 0 <= M.  M == 0 is a no-op.
  *  - Return value: BL_OK or a negative BL_ERR_* code; the message of the most
  *    recent failure on the calling thread is bitlinear_last_error().
  *  - Device-side failures (a bounded wait that ran out) set a bit in the
  *    workspace's status word; bitlinear_device_status reads and clears it.
+ *    Those of the 8-bit product set one of the device's too: bitlinear_i8_status.
  *  - A workspace starts with a 256-byte status word, which must be zero
  *    before first use (zero the workspace once after allocating it).  Calls
  *    that overlap on the GPU must not share a workspace.
@@ -423,6 +424,16 @@ int bitlinear_layer_chain(const bl_layer* layers, int n_layers, int M, int x_dty
 int bitlinear_device_status(void* workspace, void* stream);
 
 /*
+ * The 8-bit product's waits on the current device, whatever workspace their
+ * calls were given: synchronises `stream`, then returns BL_OK or
+ * BL_ERR_DEVICE_TIMEOUT if a wait of bitlinear_forward_i8 or
+ * bitlinear_forward_i8_quantized ran out since the last call, in an eager call
+ * or in a replayed graph, and forgets it.  Such a product's outputs are not
+ * complete.  Not during a capture.
+ */
+int bitlinear_i8_status(void* stream);
+
+/*
  * Exercises the device-side bounded wait: launches one block that waits on a
  * barrier nothing completes, with a limit of `limit_us` microseconds
  * (1 .. 1000000); the wait gives up, sets the status word and returns.  A
@@ -430,6 +441,8 @@ int bitlinear_device_status(void* workspace, void* stream);
  */
 int bitlinear_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int limit_us,
                                     void* stream);
+/* The same with the 8-bit product's wait, which bitlinear_i8_status reports too. */
+int bitlinear_selftest_i8_wait_timeout(void* workspace, size_t workspace_bytes, int limit_us, void* stream);
 
 /*
  * The forward of bitlinear_forward for callers that cannot allocate device

@@ -98,7 +98,9 @@ def lib() -> ctypes.CDLL:
             "bitlinear_chain_workspace_bytes": (sz, [ctypes.POINTER(bl_layer), i32, i32]),
             "bitlinear_layer_chain": (i32, [ctypes.POINTER(bl_layer), i32, i32, i32, i32, vp, sz, vp]),
             "bitlinear_device_status": (i32, [vp, vp]),
+            "bitlinear_i8_status": (i32, [vp]),
             "bitlinear_selftest_wait_timeout": (i32, [vp, sz, i32, vp]),
+            "bitlinear_selftest_i8_wait_timeout": (i32, [vp, sz, i32, vp]),
             "bitlinear_set_path": (i32, [i32]),
             "bitlinear_set_decode_split": (i32, [i32]),
             "bitlinear_set_decode_form": (i32, [i32]),
@@ -684,6 +686,18 @@ def noalloc_status(stream=None) -> int:
 def device_status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronises and returns BL_OK or BL_ERR_DEVICE_TIMEOUT (clearing the status word)."""
     return lib().bitlinear_device_status(_ptr(workspace), _stream(stream))
+
+
+def i8_status(stream=None) -> int:
+    """Synchronises ``stream`` (else the current one) and returns BL_OK or BL_ERR_DEVICE_TIMEOUT for every 8-bit product
+    on its device since the last call, those without a workspace and those of replayed graphs among them."""
+    s = stream if stream is not None else torch.cuda.current_stream()
+    with torch.cuda.device(s.device):
+        return lib().bitlinear_i8_status(ctypes.c_void_p(s.cuda_stream))
+
+
+def selftest_i8_wait_timeout(workspace: torch.Tensor, limit_us: int, stream=None) -> None:
+    _check(lib().bitlinear_selftest_i8_wait_timeout(_ptr(workspace), workspace.numel(), limit_us, _stream(stream)))
 
 
 def selftest_wait_timeout(workspace: torch.Tensor, limit_us: int, stream=None) -> None:

@@ -993,11 +993,35 @@ int bitlinear_device_status(void* workspace, void* stream) {
   return BL_OK;
 }
 
-int bitlinear_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int limit_us, void* stream) {
+int bitlinear_i8_status(void* stream) {
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
+  uint32_t word = 0;
+  e = bl::take_i8_status(&word);
+  if (e != cudaSuccess) return cuda_fail(e, "status read");
+  if (word != 0)
+    return fail(BL_ERR_DEVICE_TIMEOUT, "a device-side wait of an 8-bit product ran out of time (status 0x%x)", word);
+  return BL_OK;
+}
+
+static int check_selftest(const void* workspace, size_t workspace_bytes, int limit_us) {
   BL_TRY(check_ptr(workspace, "workspace", 256));
   if (workspace_bytes < kStatusBytes)
     return fail(BL_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, kStatusBytes);
   if (limit_us < 1 || limit_us > 1000000) return fail(BL_ERR_INVALID_ARG, "limit_us = %d not in [1, 1e6]", limit_us);
+  return BL_OK;
+}
+
+int bitlinear_selftest_i8_wait_timeout(void* workspace, size_t workspace_bytes, int limit_us, void* stream) {
+  BL_TRY(check_selftest(workspace, workspace_bytes, limit_us));
+  cudaError_t e = bl::launch_i8_wait_timeout_selftest(static_cast<uint32_t*>(workspace), limit_us,
+                                                      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "selftest launch");
+  return BL_OK;
+}
+
+int bitlinear_selftest_wait_timeout(void* workspace, size_t workspace_bytes, int limit_us, void* stream) {
+  BL_TRY(check_selftest(workspace, workspace_bytes, limit_us));
   cudaError_t e = bl::launch_wait_timeout_selftest(static_cast<uint32_t*>(workspace), limit_us,
                                                    static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "selftest launch");

@@ -68,6 +68,11 @@ struct I8Cfg {
   static_assert(kOffOut % 1024 == 0, "swizzled staging alignment");
 };
 
+// Set by every wait of this file that runs out on the device, whatever
+// workspace its call was given: a call without one has no status word that its
+// caller could read, nor has a replayed graph.
+__device__ uint32_t g_status;
+
 // Bounded wait; in the pair form giving up raises the peer's abort flag too.
 template <int CG>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const WaitCtl& ctl, uint32_t peer_abort) {
@@ -79,7 +84,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Wa
     if (global_ns() - t0 > ctl.limit_ns) {
       *ctl.abort = 1;
       if (CG == 2) st_shared_cluster_u32(peer_abort, 1u);
-      if (ctl.status) atomicOr(ctl.status, kStatusTimeout);
+      if (ctl.status) {
+        atomicOr(ctl.status, kStatusTimeout);
+        atomicOr(&g_status, kStatusTimeout);
+      }
       return false;
     }
   }
@@ -574,6 +582,20 @@ __global__ void __launch_bounds__(kThreads) i8_gemm_kernel(const __grid_constant
   }
 }
 
+// A wait that nothing ends (see launch_i8_wait_timeout_selftest).
+__global__ void i8_wait_timeout_selftest_kernel(uint32_t* status, unsigned long long limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag;
+  griddep_wait();
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bar), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+    const WaitCtl ctl{status, &abort_flag, limit_ns};
+    wait_bar<1>(smem_u32(&bar), 0, ctl, 0u);
+  }
+}
+
 bool map_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle swz, CUtensorMapDataType type) {
   EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
@@ -719,6 +741,18 @@ cudaError_t launch_i8_gemm_t(const I8Args& a, cudaStream_t stream, bool pdl) {
 }
 
 }  // namespace
+
+cudaError_t launch_i8_wait_timeout_selftest(uint32_t* status, int limit_us, cudaStream_t stream) {
+  return launch(i8_wait_timeout_selftest_kernel, dim3(1), dim3(32), 0, stream, true, status,
+                static_cast<unsigned long long>(limit_us) * 1000ull);
+}
+
+cudaError_t take_i8_status(uint32_t* word) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, g_status, sizeof(*word));
+  if (e != cudaSuccess || *word == 0) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+}
 
 cudaError_t launch_i8_gemm(const I8Args& a, cudaStream_t stream, bool pdl) {
   if (a.M <= 0) return cudaSuccess;

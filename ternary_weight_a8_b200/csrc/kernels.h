@@ -221,6 +221,11 @@ bool i8_takes_gemv(int M, int N, int K);                  // the decode kernel's
 bool i8_gemv_quantises(int M, int N, int K, int x_bf16);  // and those at which it takes raw tokens
 cudaError_t launch_i8_gemv(const I8Args& a, cudaStream_t stream, bool pdl);  // M <= kI8GemvMaxTokens
 cudaError_t launch_i8_gemm(const I8Args& a, cudaStream_t stream, bool pdl);
+// Reads and clears the current device's word of waits that ran out in
+// launch_i8_gemm's kernel, and its self-test: a wait of that kernel's own that
+// nothing ends.  (launch_i8_gemv's kernel has no waits.)
+cudaError_t take_i8_status(uint32_t* word);
+cudaError_t launch_i8_wait_timeout_selftest(uint32_t* status, int limit_us, cudaStream_t stream);
 
 // Self-test of the bounded device wait.
 cudaError_t launch_wait_timeout_selftest(uint32_t* status, int limit_us, cudaStream_t stream);

@@ -30,3 +30,29 @@ def test_activations_and_scales_change_between_calls(M, N, K):
         got.append((i, j, tb.forward_i8(wq, rows, xs[i], out_dtype=torch.float32)))
     for k, (i, j, y) in enumerate(got):
         assert torch.equal(y, want[i, j]), k
+
+
+def test_a_wait_that_runs_out_is_seen_without_a_workspace():
+    """The product's own bounded wait, with nothing to end it: the workspace and the device's word say so, eager or in a
+    replayed graph; the context stays usable."""
+    wq, ws = tb.quant_weights_i8(dev(weights(640, 2560, seed=1)))
+    x, _ = activations(47, 2560, seed=2, dtype="bf16")
+    want = tb.forward_i8(wq, ws, x)
+    assert tb.i8_status() == tb.BL_OK
+    buf = tb.new_workspace(256)
+    tb.selftest_i8_wait_timeout(buf, 2000)
+    assert tb.i8_status() == tb.BL_ERR_DEVICE_TIMEOUT and "8-bit product" in tb.last_error()
+    assert tb.i8_status() == tb.BL_OK
+    assert tb.device_status(buf) == tb.BL_ERR_DEVICE_TIMEOUT and tb.device_status(buf) == tb.BL_OK
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y = tb.forward_i8(wq, ws, x)
+        tb.selftest_i8_wait_timeout(torch.empty(256, dtype=torch.uint8, device="cuda"), 2000)
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            graph.replay()
+        assert tb.i8_status(side) == tb.BL_ERR_DEVICE_TIMEOUT
+        assert tb.i8_status(side) == tb.BL_OK
+    assert torch.equal(y, want) and torch.equal(tb.forward_i8(wq, ws, x), want)
+    assert tb.i8_status() == tb.BL_OK
