@@ -4,6 +4,7 @@ import torch
 
 import ternary_weight_a8_b200 as tb
 from parity import activations, dev, weights
+from test_gpu_i8 import _check, _codes
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,29 @@ def test_a_wait_that_runs_out_is_seen_without_a_workspace():
         assert tb.i8_status(side) == tb.BL_OK
     assert torch.equal(y, want) and torch.equal(tb.forward_i8(wq, ws, x), want)
     assert tb.i8_status() == tb.BL_OK
+
+
+# Few tokens through either kernel, sizes that automatic dispatch gives to the other one among them.
+@pytest.mark.parametrize("M,N,K", [(1, 1, 64), (1, 6912, 2560), (2, 5, 192), (5, 64, 8640), (8, 128000, 64), (8, 100, 16384),
+                                   (9, 1000, 640), (12, 12800, 2560), (16, 200, 16384), (16, 3200, 8640), (17, 16, 2560),
+                                   (24, 515, 1024), (31, 257, 64), (32, 12800, 2560), (32, 333, 28672), (32, 2560, 6912)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_both_kernels_by_force(M, N, K, dtype):
+    """Accumulators exact and outputs the documented fp32 steps, on codes and on raw tokens, whichever kernel is forced."""
+    q, s = _codes(M, K, M + K)
+    w, ws = _codes(N, K, N + K)
+    wd, wsd, qd, sd = dev(w), dev(ws), dev(q), dev(s)
+    x = activations(M, K, seed=M + K, dtype="bf16")[0].to(dtype)
+    xq, xs, _ = tb.quant_act(x)
+    out = {}
+    for path in (tb.PATH_GEMV, tb.PATH_GEMM, tb.PATH_AUTO):
+        tb.set_path(path)
+        try:
+            y, acc = tb.forward_i8_quantized(wd, wsd, qd, sd, out_dtype=dtype, acc_out=True)
+            raw = tb.forward_i8(wd, wsd, x, out_dtype=torch.float32, acc_out=True)
+        finally:
+            tb.set_path(tb.PATH_AUTO)
+        _check(y, acc, q, s, w, ws)
+        _check(raw[0], raw[1], xq.cpu().numpy(), xs.cpu().numpy(), w, ws)
+        out[path] = y
+    assert torch.equal(out[tb.PATH_GEMV], out[tb.PATH_GEMM]) and torch.equal(out[tb.PATH_GEMV], out[tb.PATH_AUTO])
