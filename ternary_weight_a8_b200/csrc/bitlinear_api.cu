@@ -500,7 +500,7 @@ int bitlinear_forward_i8_quantized(const int8_t* wq, const float* wscale, int N,
                      {workspace, kStatusBytes, "workspace"}, {y, m * n * (y_dtype == BL_BF16 ? 2 : 4), "y"},
                      {acc_out, m * n * 4, "acc_out"}};
   for (int i = 4; i < 7; ++i) BL_TRY(check_apart(sp[i], sp, i));
-  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, K, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
                               acc_out, static_cast<uint32_t*>(workspace)},
                    static_cast<cudaStream_t>(stream));
 }
@@ -528,14 +528,13 @@ int bitlinear_forward_i8(const int8_t* wq, const float* wscale, int N, int K, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
   float* scale = reinterpret_cast<float*>(ws + l.scale);
-  const int ldq = code_pitch(K);
   if (i8_gemv(M, N, K) && bl::i8_gemv_quantises(M, N, K, x_dtype == BL_BF16))
-    return launch_i8(bl::I8Args{wq, wscale, N, K, M, nullptr, 0, nullptr, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+    return launch_i8(bl::I8Args{wq, wscale, N, K, M, nullptr, nullptr, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
                                 acc_out, static_cast<uint32_t*>(workspace), x, x_dtype == BL_BF16},
                      s);
-  cudaError_t e = bl::launch_row_codes(x, x_dtype == BL_BF16, M, K, ldq, xq, scale, s, true);
+  cudaError_t e = bl::launch_row_codes(x, x_dtype == BL_BF16, M, K, xq, scale, s, true);
   if (e != cudaSuccess) return cuda_fail(e, "activation codes launch");
-  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, ldq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
+  return launch_i8(bl::I8Args{wq, wscale, N, K, M, xq, scale, y, y_dtype == BL_BF16 ? bl::kOutBF16 : bl::kOutF32,
                               acc_out, static_cast<uint32_t*>(workspace)},
                    s);
 }

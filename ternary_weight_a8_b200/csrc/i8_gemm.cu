@@ -654,7 +654,7 @@ cudaError_t launch_t(const I8Args& a, int bn, int split, cudaStream_t stream, bo
   using C = I8Cfg<TY, CG>;
   const int rows_a = a.M < kBM ? (a.M + 7) / 8 * 8 : kBM;
   CUtensorMap tx, tw, ty = {};
-  if (!map_2d(&tx, a.xq, a.K, a.M, a.ldx, kBK, rows_a, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+  if (!map_2d(&tx, a.xq, a.K, a.M, a.K, kBK, rows_a, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
       !map_2d(&tw, a.wq, a.K, a.N, a.K, kBK, bn / CG, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8))
     return cudaErrorInvalidValue;
   const uint64_t pitch = static_cast<uint64_t>(a.N) * sizeof(TY);

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * kGvWarps, BPS)
     wp[i] = reinterpret_cast<const uint8_t*>(P.wq) + static_cast<size_t>(min(n0 + g + 8 * i, P.N - 1)) * P.K + 16 * t;
   // Raw tokens' codes lie an odd number of 64 bytes apart, so that the pieces
   // of two neighbouring tokens fall into different halves of the banks.
-  const int pitch = kRaw ? P.K | 64 : P.ldx;
+  const int pitch = kRaw ? P.K | 64 : P.K;
   const uint8_t* xp[TG];
 #pragma unroll
   for (int j = 0; j < TG; ++j)

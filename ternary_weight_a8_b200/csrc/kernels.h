@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <type_traits>
 
 namespace bl {
 
@@ -193,24 +192,23 @@ cudaError_t launch_ste_backward(const uint8_t* packed, const float* gamma, int N
                                 uint32_t* status, cudaStream_t stream);
 
 // The codes of rows of activations, as launch_act_quant makes them (no code
-// sums); rows of ldq bytes, zero past K.
-cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int ldq, int8_t* xq, float* scale,
-                             cudaStream_t stream, bool pdl);
+// sums, rows of K bytes).
+cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int8_t* xq, float* scale, cudaStream_t stream,
+                             bool pdl);
 
 // The 8-bit product: y = acc / (s[m] * ws[n]) with acc = sum_k xq[m][k] * wq[n][k] in int32.
 struct I8Args {
   const int8_t* wq;      // [N][K]
   const float* wscale;   // [N]
   int N, K, M;
-  const int8_t* xq;      // [M][ldx]
-  int ldx;               // >= K, a multiple of 16
+  const int8_t* xq;      // [M][K]
   const float* scale;    // [M]
   void* y;               // [M][N]
   int y_type;            // OutType
   int32_t* acc_out;      // [M][N] or null
   uint32_t* status;
   // Raw tokens [M][K], or null: the decode kernel then quantises them itself
-  // (i8_gemv_quantises) and xq, ldx and scale are not used.
+  // (i8_gemv_quantises) and xq and scale are not used.
   const void* x = nullptr;
   int x_bf16 = 0;
 };

@@ -440,9 +440,9 @@ cudaError_t launch_add_rmsnorm_quant_t(const AddNormParams& P, cudaStream_t stre
 // ---------------------------------------------------------------------------
 struct CodesParams {
   const void* x;
-  int8_t* xq;  // rows of ldq bytes, zero past K
+  int8_t* xq;
   float* scale;
-  int M, K, ldq;
+  int M, K;
 };
 
 template <typename T, int C>
@@ -458,8 +458,7 @@ __global__ void __launch_bounds__(512, C == 4 || C == 0 ? 2 : 3) row_codes_kerne
   griddep_wait();
   if (m >= P.M) return;  // the whole group: its named barrier is its own
   const uint4* xr = reinterpret_cast<const uint4*>(static_cast<const T*>(P.x) + static_cast<size_t>(m) * P.K);
-  int8_t* qr = P.xq + static_cast<size_t>(m) * P.ldq;
-  for (int c = P.K + 16 * tid; c < P.ldq; c += 16 * step) *reinterpret_cast<uint4*>(qr + c) = make_uint4(0, 0, 0, 0);
+  int8_t* qr = P.xq + static_cast<size_t>(m) * P.K;
 
   constexpr int CR = C > 0 ? C : 1;
   uint4 keep[CR];
@@ -1240,10 +1239,10 @@ cudaError_t launch_add_rmsnorm_quant(const void* x, const void* residual, int x_
                 : launch_add_rmsnorm_quant_t<float>(P, stream, pdl);
 }
 
-cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int ldq, int8_t* xq, float* scale,
-                             cudaStream_t stream, bool pdl) {
+cudaError_t launch_row_codes(const void* x, int x_bf16, int M, int K, int8_t* xq, float* scale, cudaStream_t stream,
+                             bool pdl) {
   if (M <= 0) return cudaSuccess;
-  const CodesParams P{x, xq, scale, M, K, ldq};
+  const CodesParams P{x, xq, scale, M, K};
   return x_bf16 ? launch_row_codes_t<__nv_bfloat16>(P, stream, pdl) : launch_row_codes_t<float>(P, stream, pdl);
 }
 
