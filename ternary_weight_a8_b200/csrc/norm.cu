@@ -649,9 +649,10 @@ __device__ __forceinline__ f32x2 warp_sum2(f32x2 v) {
 // A group of W warps takes tokens group0, group0 + groups_total, ...; a
 // thread owns the same C chunks of every token (kFull: all of them exist), so
 // the gain's gradient is summed in its registers and written once per block.
-// The two sums over a
-// token run as one pair of fp32 (trees of at most 26 steps): at 16 warps a
-// token, sums and 1 / rms in double were half of the kernel's instructions.
+// The two sums over a token run as one pair of fp32, through at most 31 steps
+// (16 fused ones of a thread's halves, their join, 5 shuffles, up to 4 places
+// of a cluster's warps and 5 shuffles): at 16 warps a token, sums and 1 / rms
+// in double were half of the kernel's instructions.
 // A token of more than 1024 chunks is shared by a cluster (kCluster: C chunks
 // of 32 W threads in each of its CTAs), whose sums meet in every CTA's shared
 // memory.  z and dv of the next tokens are under way in shared memory, where a

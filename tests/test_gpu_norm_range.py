@@ -88,3 +88,28 @@ def test_statistics_outside_of_fp32_in_bf16(M, K, dtype):
     bar = U * (44 * terms + depth * dots) + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -8) + 2.0 ** -133
     err = np.abs(dz.float().cpu().numpy().astype(np.float64) - want)
     assert (err <= bar).all() and not dz[1].any()
+
+
+@pytest.mark.parametrize("M,K,dtype", [(1, 64, torch.bfloat16), (20000, 192, torch.bfloat16), (3001, 2560, torch.bfloat16),
+                                       (777, 3200, torch.float32), (2500, 8192, torch.float32), (700, 28672, torch.bfloat16),
+                                       (700, 40960, torch.float32), (300, 65536, torch.float32),
+                                       (300, 65536 + 64, torch.float32)])
+def test_gain_gradient_against_its_own_depth(M, K, dtype):
+    """A term dnorm n is off by 23 u at most (r, n and the fused step); then it passes the chain over a group's tokens, at
+    most ceil(M / rows) of them, up to 8 groups of a block, and of the closing kernel a thread's ceil(rows / 128) rows,
+    two shuffles and 32 warps.  The rows of partial sums are counted in the workspace, where no sum is a NaN."""
+    gen = torch.Generator("cuda").manual_seed(M)
+    z, d = (torch.randn((M, K), device="cuda", generator=gen).to(dtype) for _ in range(2))
+    g = dev(_gain(K, K))
+    need = tb.add_rmsnorm_backward_workspace_bytes(M, K, dtype)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    _, dgain = tb.add_rmsnorm_backward(z, d, g, eps=1e-5, workspace=ws)
+    part = ws[256:256 + (need - 256) // (4 * K) * 4 * K].view(torch.int32).view(-1, K)
+    rows = int((part != -1).all(1).sum())
+    assert 1 <= rows <= M
+    zd, dd = z.double(), d.double()
+    n = zd / ((zd * zd).mean(1, keepdim=True) + float(np.float32(1e-5))).sqrt()
+    depth = 23 + -(-M // rows) + 8 + -(-rows // 128) + 2 + 32
+    bar = U * depth * (dd * n).abs().sum(0)
+    err = (dgain.double() - (dd * n).sum(0)).abs()
+    assert (err <= bar).all(), (rows, float((err / bar).max()))
