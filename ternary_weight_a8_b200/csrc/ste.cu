@@ -12,8 +12,8 @@
 // xhat is taken as the backward stores it, bf16(q / s).
 //
 // Both products run on one bf16 tcgen05 GEMM, D = alpha * A . B^T with A and
-// B K-major (row-major along the summed index), fed by three layout kernels:
-// t^T as bf16 (-1, 0, 1 exactly) from the packed weights, dy^T, and xhat^T.
+// B K-major (row-major along the summed index), fed by a layout kernel that
+// writes t^T as bf16 (-1, 0, 1 exactly) from the packed weights, dy^T and xhat^T.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -23,24 +23,37 @@
 namespace bl {
 
 // ---------------------------------------------------------------------------
-// Layout kernels: 64 x 64 tiles through shared memory.
+// The layouts: 64 x 64 tiles through shared memory, a block for each tile of
+// the three matrices.  One launch: every kernel of the chain has to wait for
+// the one before it (a GEMM's wait is for the preceding kernel alone, so what
+// came before the call is complete only if that kernel has waited for it), and
+// three launches that each wait took 207 us at 2048 x 2560 -> 6912 with the
+// GEMMs, this one 184 (16 bytes a thread; 210 with 2).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 64;
 
+struct LayoutArgs {
+  const uint32_t* packed;     // [N][K/16]
+  const __nv_bfloat16* dy;    // [M][N]
+  const int8_t* xq;           // [M][K]
+  const float* scale;         // [M]
+  int M, N, K;
+  __nv_bfloat16* tt;          // [K][N]
+  __nv_bfloat16* dyt;         // [N][M]
+  __nv_bfloat16* xht;         // [K][M]
+  int n_t, n_dy;              // blocks of t^T and of dy^T; the rest are xhat^T's
+};
+
+typedef __nv_bfloat16 LayoutTile[kTile][kTile + 2];  // padded
+
 // tt[k][n] = t[n][k] as bf16, from packed [N][K/4] (element 16g+4j+b in byte b, bits 2j..2j+1 of word g).
-// The wait is also what the GEMM behind this kernel relies on: its own wait is
-// for this kernel alone, so dy is complete only if this one has waited for it.
-__global__ void __launch_bounds__(256) unpack_transpose_kernel(const uint32_t* packed, int N, int K, __nv_bfloat16* tt) {
-  __shared__ __nv_bfloat16 tile[kTile][kTile + 2];  // [k][n], padded
-  griddep_launch_dependents();
-  griddep_wait();  // tt may still be read by the preceding kernel
-  const int n0 = blockIdx.y * kTile, k0 = blockIdx.x * kTile;
-  const int words = K / 16;
+__device__ __forceinline__ void unpack_tile(const LayoutArgs& A, int k0, int n0, LayoutTile& tile) {  // [k][n]
+  const int N = A.N, K = A.K, words = K / 16;
   // 64 rows x 4 words (64 inputs) of the packed tile: one word per thread.
   const int r = threadIdx.x >> 2, wi = threadIdx.x & 3;
   const int n = n0 + r;
   uint32_t w = 0x55555555u;  // code 1 (t = 0) outside the matrix
-  if (n < N) w = __ldcg(packed + static_cast<size_t>(n) * words + k0 / 16 + wi);
+  if (n < N) w = __ldcg(A.packed + static_cast<size_t>(n) * words + k0 / 16 + wi);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -49,46 +62,76 @@ __global__ void __launch_bounds__(256) unpack_transpose_kernel(const uint32_t* p
       tile[16 * wi + 4 * j + b][r] = __float2bfloat16_rn(static_cast<float>(code - 1));
     }
   __syncthreads();
-  // Out: 64 rows k of 64 n (128 bytes), two bf16 per thread per step.
-  for (int i = threadIdx.x; i < kTile * kTile / 2; i += blockDim.x) {
-    const int kr = i / (kTile / 2), c = 2 * (i % (kTile / 2));
+  // Out: 64 rows k of 64 n (128 bytes), eight bf16 per thread per step.
+#pragma unroll
+  for (int i = threadIdx.x; i < kTile * kTile / 8; i += 256) {
+    const int kr = i / (kTile / 8), c = 8 * (i % (kTile / 8));
     const int nn = n0 + c;
     if (k0 + kr < K && nn < N) {
-      __nv_bfloat162 v;
-      v.x = tile[kr][c];
-      v.y = tile[kr][c + 1];
-      *reinterpret_cast<__nv_bfloat162*>(tt + static_cast<size_t>(k0 + kr) * N + nn) = v;
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(&tile[kr][c]);
+      *reinterpret_cast<uint4*>(A.tt + static_cast<size_t>(k0 + kr) * N + nn) = make_uint4(row[0], row[1], row[2], row[3]);
     }
   }
 }
 
-// out[c][r] = f(in[r][c]) for a [R][C] bf16 matrix, or (xhat) bf16(q[r][c] / s[r]) from int8 codes.
-template <bool kFromCodes>
-__global__ void __launch_bounds__(256) transpose_kernel(const void* in, const float* s, int R, int C, __nv_bfloat16* out) {
-  __shared__ __nv_bfloat16 tile[kTile][kTile + 2];  // [r][c], padded
-  griddep_launch_dependents();
-  griddep_wait();  // the input may be the preceding kernel's output; out may still be read by it
-  const int r0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
-  for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
-    const int rr = i / kTile, cc = i % kTile;
-    const int r = r0 + rr, c = c0 + cc;
-    __nv_bfloat16 v = __float2bfloat16_rn(0.0f);
-    if (r < R && c < C) {
-      if constexpr (kFromCodes) {
-        const int8_t q = static_cast<const int8_t*>(in)[static_cast<size_t>(r) * C + c];
-        v = __float2bfloat16_rn(__fdiv_rn(static_cast<float>(q), __ldcg(s + r)));
-      } else {
-        v = static_cast<const __nv_bfloat16*>(in)[static_cast<size_t>(r) * C + c];
-      }
-    }
-    tile[rr][cc] = v;
+// out[c][r] = in[r][c] of an [R][C] matrix, R and C multiples of 8; in(r, c)
+// gives the eight bf16 of row r from column c on, in pairs.
+template <typename F>
+__device__ __forceinline__ void transpose_tile(F&& in, int R, int C, __nv_bfloat16* out, int r0, int c0,
+                                               LayoutTile& tile) {  // [r][c]
+#pragma unroll
+  for (int i = threadIdx.x; i < kTile * kTile / 8; i += 256) {
+    const int rr = i / (kTile / 8), cc = 8 * (i % (kTile / 8));
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r0 + rr < R && c0 + cc < C) v = in(r0 + rr, c0 + cc);
+    uint32_t* t = reinterpret_cast<uint32_t*>(&tile[rr][cc]);
+    t[0] = v.x;
+    t[1] = v.y;
+    t[2] = v.z;
+    t[3] = v.w;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kTile * kTile; i += blockDim.x) {
-    const int cc = i / kTile, rr = i % kTile;
-    const int r = r0 + rr, c = c0 + cc;
-    if (r < R && c < C) out[static_cast<size_t>(c) * R + r] = tile[rr][cc];
+#pragma unroll
+  for (int i = threadIdx.x; i < kTile * kTile / 8; i += 256) {
+    const int cc = i / (kTile / 8), rr = 8 * (i % (kTile / 8));
+    __align__(16) __nv_bfloat162 v[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = __nv_bfloat162(tile[rr + 2 * p][cc], tile[rr + 2 * p + 1][cc]);
+    if (r0 + rr < R && c0 + cc < C)
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(c0 + cc) * R + r0 + rr) = *reinterpret_cast<const uint4*>(v);
   }
+}
+
+__global__ void __launch_bounds__(256) layout_kernel(const LayoutArgs A) {
+  __shared__ __align__(16) LayoutTile tile;
+  griddep_launch_dependents();
+  griddep_wait();  // dy, codes and scales may be the preceding kernel's; the scratch may still be read by it
+  const int kt = (A.K + kTile - 1) / kTile, nt = (A.N + kTile - 1) / kTile;
+  int b = blockIdx.x;
+  if (b < A.n_t) {
+    unpack_tile(A, b % kt * kTile, b / kt * kTile, tile);
+    return;
+  }
+  b -= A.n_t;
+  if (b < A.n_dy) {
+    transpose_tile(
+        [&](int r, int c) { return __ldcg(reinterpret_cast<const uint4*>(A.dy + static_cast<size_t>(r) * A.N + c)); },
+        A.M, A.N, A.dyt, b / nt * kTile, b % nt * kTile, tile);
+    return;
+  }
+  b -= A.n_dy;
+  transpose_tile(
+      [&](int r, int c) {
+        const uint2 q = __ldcg(reinterpret_cast<const uint2*>(A.xq + static_cast<size_t>(r) * A.K + c));
+        const float s = __ldcg(A.scale + r);
+        auto pair = [&](uint32_t w, int at) {
+          const float lo = static_cast<float>(static_cast<int8_t>(w >> at)), hi = static_cast<float>(static_cast<int8_t>(w >> (at + 8)));
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+          return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        return make_uint4(pair(q.x, 0), pair(q.x, 16), pair(q.y, 0), pair(q.y, 16));
+      },
+      A.M, A.K, A.xht, b / kt * kTile, b % kt * kTile, tile);
 }
 
 // ---------------------------------------------------------------------------
@@ -313,25 +356,19 @@ cudaError_t launch_ste_backward(const uint8_t* packed, const float* gamma, int N
   __nv_bfloat16* dyt = reinterpret_cast<__nv_bfloat16*>(scratch + r256(static_cast<size_t>(K) * N * 2));
   __nv_bfloat16* xht = reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<uint8_t*>(dyt) +
                                                        r256(static_cast<size_t>(N) * M * 2));
-  cudaError_t e = cudaSuccess;
+  auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
+  LayoutArgs a{reinterpret_cast<const uint32_t*>(packed), static_cast<const __nv_bfloat16*>(dy), xq, scale, M, N, K,
+               tt, dyt, xht, dx ? tiles(K) * tiles(N) : 0, dw ? tiles(M) * tiles(N) : 0};
+  const int blocks = a.n_t + a.n_dy + (dw ? tiles(M) * tiles(K) : 0);
+  cudaError_t e = launch(layout_kernel, dim3(blocks), dim3(256), 0, stream, true, a);
+  if (e != cudaSuccess) return e;
   if (dx) {
     // dx[M][K] = gamma * dy[M][N] . (t^T)[K][N]^T
-    e = launch(unpack_transpose_kernel, dim3((K + kTile - 1) / kTile, (N + kTile - 1) / kTile), dim3(256), 0, stream,
-               true, reinterpret_cast<const uint32_t*>(packed), N, K, tt);
-    if (e != cudaSuccess) return e;
-    e = launch_gemm_bf16(static_cast<const __nv_bfloat16*>(dy), tt, M, K, N, 1.0f, gamma, dx, dx_bf16, status, stream);
+    e = launch_gemm_bf16(a.dy, tt, M, K, N, 1.0f, gamma, dx, dx_bf16, status, stream);
     if (e != cudaSuccess) return e;
   }
-  if (dw) {
-    // dW[N][K] = (dy^T)[N][M] . (xhat^T)[K][M]^T
-    e = launch(transpose_kernel<false>, dim3((N + kTile - 1) / kTile, (M + kTile - 1) / kTile), dim3(256), 0, stream,
-               true, dy, static_cast<const float*>(nullptr), M, N, dyt);
-    if (e != cudaSuccess) return e;
-    e = launch(transpose_kernel<true>, dim3((K + kTile - 1) / kTile, (M + kTile - 1) / kTile), dim3(256), 0, stream,
-               true, static_cast<const void*>(xq), scale, M, K, xht);
-    if (e != cudaSuccess) return e;
-    e = launch_gemm_bf16(dyt, xht, N, K, M, 1.0f, nullptr, dw, false, status, stream);
-  }
+  // dW[N][K] = (dy^T)[N][M] . (xhat^T)[K][M]^T
+  if (dw) e = launch_gemm_bf16(dyt, xht, N, K, M, 1.0f, nullptr, dw, false, status, stream);
   return e;
 }
 

@@ -65,5 +65,5 @@ def test_every_dependent_kernel_waits_for_the_kernel_before_it():
             for kernel, body in _kernels(_code(name)):
                 seen.add(kernel)
                 assert "griddep_wait()" in body, "%s: %s" % (name, kernel)
-    assert {"unpack_transpose_kernel", "transpose_kernel", "gemm_bf16_kernel", "i8_gemm_kernel", "gemv_group_kernel",
+    assert {"layout_kernel", "gemm_bf16_kernel", "i8_gemm_kernel", "gemv_group_kernel",
             "gemm_kernel", "add_rmsnorm_backward_kernel", "act_quant_kernel"} <= seen
