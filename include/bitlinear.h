@@ -140,7 +140,10 @@ int bitlinear_rmsnorm_quant(const void* x, int x_dtype, int M, int K, const floa
  * activation quantisation in one pass: what every block of a pre-norm model
  * does between one BitLinear and the next.
  *   z = x + residual (fp32 sum, rounded to x_dtype and stored), and then
- *   exactly bitlinear_rmsnorm_quant of z, bit for bit.
+ *   bitlinear_rmsnorm_quant of z, step for step: equal bit for bit, up to the
+ *   order in which the squares are summed in double.  That order can change
+ *   the fp32 root's last bit where the sum is not exact (fp32 tokens, bf16
+ *   tokens of wide range), once in some millions of tokens.
  *   x, residual  device [M][K] of x_dtype (BL_F32 or BL_BF16); 16-byte aligned.
  *   z            device [M][K] of x_dtype out; may be x or residual itself
  *                (the sum in place), and otherwise overlaps neither.

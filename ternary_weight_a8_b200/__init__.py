@@ -358,7 +358,7 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor, gain: torch.Tenso
                       z: torch.Tensor | None = None, x_norm=None, xq=None, scale=None, rowsum=None, stream=None):
     """z = x + residual, RMSNorm of z and its per-token quantisation in one pass: returns (z, xq, scale, rowsum),
     with the normalised activations after z when ``x_norm`` is True or a tensor.  ``z`` may be ``x`` or
-    ``residual`` (the sum in place).  The codes equal ``rmsnorm_quant``'s on z."""
+    ``residual`` (the sum in place).  The codes equal ``rmsnorm_quant``'s on z (up to the order of a sum in double)."""
     M, K = x.shape
     dt = x.dtype
     code = _dtype_code(dt)

@@ -19,13 +19,17 @@
 // the status word, raises the abort flags and the block winds down.
 //
 // What bounds it: with many tokens the tensor cores (2048 tokens, 8192 ->
-// 28672: 295 - 303 us, 3.18 - 3.26 POPS, where the library's 8192^3 product
-// runs at 2.85; 2560 -> 6912: 27.4 us, 2.64 POPS); with up to 128 tokens and
-// large matrices the weights' stream (32 tokens, 8192 -> 28672: 43 us, 5.5
-// TB/s; 2560 -> 128000: 55 us, 6.0 TB/s), which is why the tile width is free:
-// the tiles should come out even over the SMs (448 tiles of 64 or 224 of 128
-// channels for 148 SMs leave a quarter of the time idle, 138 of 208 none);
-// and in between the latency of a tile's k-blocks, which the split shortens.
+// 28672: 299 - 314 us by the power that is left, 3.06 - 3.22 POPS, where the
+// library's 8192^3 product runs at 2.85; 2560 -> 6912: 28 us, 2.6 POPS; with
+// fp32 outputs 337 and 31 us), as far as the pairs' whole tiles fill their last
+// round: 2048 tokens, 2560 -> 2560 are 80 tiles on 74 pairs and take 19.0 us,
+// 44% of the rate; with up to 128 tokens and large matrices the weights'
+// stream (32 tokens, 8192 -> 28672: 44.4 us, 5.3 TB/s; 2560 -> 128000: 55 us,
+// 6.0 TB/s), which is why the tile width is free: 448 tiles of 64 or 224 of
+// 128 channels for 148 SMs leave a quarter of the time idle (the model takes
+// 224 channels for 28672, 128 tiles that leave 20 SMs without one, as the
+// stream bounds them all the same); and in between the latency of a tile's
+// k-blocks, which the split shortens.
 // An MMA of one CTA holds the tensor core for about 130 clocks whatever its
 // width, so narrow tiles are only as fast as wide ones.
 #include <cuda.h>

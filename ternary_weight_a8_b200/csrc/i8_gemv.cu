@@ -17,10 +17,12 @@
 // (32-byte loads, which touch half as many lines at a time, were faster on
 // short calls by up to 8% and slower on the long ones by 10 to 20%).
 //
-// Measured, the weights new in every call: 1 token, 2560 -> 128000: 51.3 us
-// (6.4 TB/s, 97% of the copy rate); 8 tokens, 8192 -> 28672: 38.4 us (93%);
-// 1 token, 28672 -> 8192: 37.3 us; short calls are latency: 1 token, 2560 ->
-// 6912: 4.9 us, of which the weights need 2.7 and an empty launch 2.
+// Measured, the weights new in every call: 1 token, 2560 -> 128000: 50.5 us
+// (6.5 TB/s, 99% of the copy rate); 8 tokens, 8192 -> 28672: 37.8 us (95%);
+// 1 token, 28672 -> 8192: 37.8 us; short calls are latency: 1 token, 2560 ->
+// 6912: 4.6 us, of which the weights need 2.7 and an empty launch 2.  (The
+// sweeps behind the rules below were taken when a block still read its scales
+// last; every form has become 1 to 8% faster since.)
 #include <cuda_bf16.h>
 #include <type_traits>
 

@@ -7,7 +7,9 @@
 //   r = fp32(1 / sqrt(mean_k z^2 + eps))      squares summed in double, as rmsnorm_quant does
 //   v = T((z * r) * g)                        fp32 products
 //   s = 127 / max(max_k |v|, 1e-5),  q = clamp(rint(v * s)),  rowsum = sum_k q
-// so the codes equal rmsnorm_quant's on z bit for bit.
+// so the codes equal rmsnorm_quant's on z bit for bit, up to the order of the
+// sum in double: where that is not exact its last bits differ, and once in some
+// millions of tokens the fp32 root with them.
 //
 // Backward, with n = z * r and the quantisation as the identity
 // (straight-through), for the gradient dv of v and dz_in of z:
@@ -20,9 +22,9 @@
 // arithmetic has to stay small: sums in bf16 pairs, packed fp32 products,
 // maxima as integers, codes by an addition, 1 / rms by Newton's method.
 // 8192 x 8192 bf16 forward took 126 us in scalar arithmetic, 78 - 80 in pairs
-// and takes 72 - 75 (96 - 99% of the copy rate, by where the tensors lie) with
-// the next tokens read ahead into L2; backward 167 us, 96 and 92 (89%).  2048
-// x 2560 (one wave, 5.6 us of traffic) takes 11.6 us forward and 15.7 backward,
+// and takes 74 - 76 (94 - 96% of the copy rate, by where the tensors lie) with
+// the next tokens read ahead into L2; backward 167 us, 96 and 91 (90%).  2048
+// x 2560 (one wave, 5.6 us of traffic) takes 11.2 us forward and 15.9 backward,
 // of which 5 are the closing kernel's boundary and its sum.
 #include <cuda_bf16.h>
 #include <math.h>

@@ -44,6 +44,43 @@ def test_training_step(M, K):
     assert ((want[0][2].double() - dx).abs() <= 2.0 ** -24 * (2 * K + 4) * terms).all()
 
 
+@pytest.mark.parametrize("M,K", [(8, 192), (304, 2560)])
+def test_training_step_captured(M, K):
+    """The same calls in one graph, replayed on inputs that change between replays."""
+    packed, gamma = tb.pack_weights(dev(weights(K, K, seed=1)))
+    g = torch.ones(K, device="cuda")
+    ws = [tb.new_workspace(tb.ste_workspace_bytes(M, K, K)) for _ in range(2)]
+    x, d = (torch.zeros((M, K), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step(wait=lambda: None):
+        z, q, s, _ = tb.add_rmsnorm_quant(x, x, g)
+        wait()
+        dz, dg = tb.add_rmsnorm_backward(z, d, g, dz_in=x)
+        wait()
+        dx, dw = tb.ste_backward(packed, gamma, K, dz, q, s, workspace=ws[0])
+        wait()
+        dn, dg2 = tb.add_rmsnorm_backward(z, dx, g)
+        wait()
+        return dz, dg, dx, dw, dn, dg2, tb.ste_backward(packed, gamma, K, dn, q, s, dx=False, workspace=ws[1])[1]
+
+    inputs = [(activations(M, K, seed=20 + k, dtype="bf16")[0], activations(M, K, seed=30 + k, dtype="bf16")[0] * 0.1 ** k)
+              for k in range(3)]
+    want = []
+    for a, b in inputs:
+        x.copy_(a)
+        d.copy_(b)
+        want.append([t.clone() for t in step(torch.cuda.synchronize)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(9):
+        x.copy_(inputs[i % 3][0])
+        d.copy_(inputs[i % 3][1])
+        graph.replay()
+        for j, (a, b) in enumerate(zip(out, want[i % 3])):
+            assert torch.equal(a, b), (i, j)
+
+
 def _ternary(packed, K):
     """Ternary values [N][K] of packed weights (element 16 g + 4 j + b in byte b of word g, bits 2 j and 2 j + 1)."""
     words = packed.reshape(packed.shape[0], K // 16, 4)  # [N][g][b]
