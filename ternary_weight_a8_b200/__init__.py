@@ -332,7 +332,7 @@ class _Call:
         else:
             capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
-            # Not zeroed: the calls only ever add to the status word, and nobody reads this one's.
+            # Not zeroed: the calls only ever add to the status word, and i8_status reads the device's.
             ws = self.new((max(int(nbytes), 256),), torch.uint8)
         else:
             cache = _WS_LOCAL.__dict__

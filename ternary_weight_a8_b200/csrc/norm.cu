@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kRoom ? 256 : 512, (C == 4 && !kRoom) || C == 
   // they are used: as many early as the registers take without spilling (all
   // where they are used: 4096 x 1280 fp32 16.1 us, 13.3 with all first; 2048 x
   // 5120 bf16, four chunks with room, 18.1, 16.0 with 2 and 4, 17.2 with all
-  // first; 2048 x 2560 bf16, five chunks, 12.5, 11.2 with 3, 12.4 with 2 and 4;
+  // first; 2048 x 2560 bf16, five chunks, 12.5, 11.2 with 3, 12.4 with 1 and 4;
   // 64 x 8192 bf16, two chunks of 40 registers, 5.1 with none and 5.7 with any).
   constexpr int kGainFirst = sizeof(T) == 4 || C <= 1 ? C : C == 2 ? 0 : C == 4 ? (kRoom ? 2 : kFull ? 0 : 1) : 3;
   constexpr int kGainNext = kRoom && C == 4 ? 4 : kGainFirst;
